@@ -86,6 +86,9 @@ typedef enum {
 #define PQ_ERR_DEVICE (-6)   /* current device is not compute capability 10.3 (sm_103) */
 #define PQ_ERR_LAUNCH (-7)   /* a launch, or the pool allocation before it, failed */
 #define PQ_ERR_KERNEL (-8)   /* unknown kernel id passed to pq_gemv_kernel */
+#define PQ_ERR_DTYPE (-9)    /* unknown element type (pq_kv_*, pq_attn) */
+#define PQ_ERR_LAYOUT (-10)  /* head size, head counts, page size or rotated size not supported */
+#define PQ_ERR_WS (-11)      /* pq_attn's workspace is smaller than pq_attn_ws_bytes */
 
 /*
  * y[b][r] = sum_i w(r, i) * x[b][i]   for b < batch, r < n_out.
@@ -269,6 +272,116 @@ int pq_selftest_wait_timeout(unsigned limit_us, struct CUstream_st *stream);
  */
 int pq_gemv_noalloc(pq_fmt fmt, const void *w_blocks, int n_out, int k,
                     const float *x, int batch, float *y, struct CUstream_st *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key/value cache in 8 bits, and the attention that reads it.
+ *
+ * What stands between a layer's QKV projection and its O projection
+ * (grouped-query attention over a cache of keys and values: PESTI README,
+ * "Conformance"; ember pull request, attention.rs).  The cache holds int8
+ * codes with one f32 scale per page and kv head, for K and for V separately:
+ * a quarter of the bytes of an f32 cache, plus 8 / (page * d) bytes per value.
+ *
+ *   k, v              device int8 [n_pages][n_kv][page][d], 16-byte aligned;
+ *                     value = scale * code
+ *   k_scale, v_scale  device f32 [n_pages][n_kv]
+ *   table             device int32 [n_seq][table_ld]: table[s][j] is the page
+ *                     of tokens j*page .. j*page+page-1 of sequence s; an
+ *                     entry outside [0, n_pages) means that there is none
+ *   len               device int32 [n_seq]: tokens of each sequence, those of
+ *                     the present call included
+ * page is 16, 32, 64 or 128; d a multiple of 16 from 16 to 256; n_q a multiple
+ * of n_kv.  The buffers are the caller's; the handle is plain host memory,
+ * read during the call only, so table and len may be rewritten in place
+ * between calls.
+ *
+ * Rows.  A call's rows (the new tokens, or the queries) lie sequence by
+ * sequence: those of sequence s are rows row_start[s] .. row_start[s+1]-1
+ * (device int32 [n_seq+1], from 0 to n_rows, not decreasing).  row_start may
+ * be NULL: one row per sequence, n_rows == n_seq.  Row i of the m rows of
+ * sequence s is the token at position len[s] - m + i.  A position below 0, or
+ * one whose page the table does not have, is in no cache: such a token is not
+ * written, not visible, and reads as zeros.  So an idle slot of a batch has
+ * len 0.  Table, len and row_start are read on the device: entries out of
+ * range are never followed.
+ */
+typedef enum { PQ_F32 = 0, PQ_F16 = 1, PQ_BF16 = 2 } pq_dtype;
+
+typedef struct pq_kv_cache {
+    signed char *k, *v;
+    float *k_scale, *v_scale;
+    const int *table;
+    const int *len;
+    int n_pages, n_kv, page, d, n_seq, table_ld;
+} pq_kv_cache;
+
+#define PQ_ROPE_HALF 0   /* pairs (i, i + rot/2) */
+#define PQ_ROPE_PAIR 1   /* pairs (2i, 2i + 1) */
+
+/*
+ * Append keys and values, rotated to their positions on the way.
+ *
+ *   k, v       device [n_rows][n_kv * d] of type dt, row strides ldk, ldv in
+ *              elements (columns of a fused QKV output pass as they are)
+ *   q, q_out   NULL, or device [n_rows][n_q * d] with row strides ldq, ldqo:
+ *              q is rotated too and stored to q_out; q_out may be q itself
+ *   rope_cos, rope_sin  device f32 [n_pos][rot/2], 16-byte aligned: row p is
+ *              the angle's cosine and sine at position p, for each pair.  The
+ *              first rot elements of every head are rotated (rot a multiple of
+ *              16, at most d; 0: none, and the tables may be NULL):
+ *                  a' = a c - b s,   b' = a s + b c
+ *              with every product and the difference or sum rounded to f32.
+ *              A position below 0 rotates as 0; at n_pos or above it gives NaN.
+ * Quantization, per page and kv head, in f32: t = max|new values in the
+ * page| / 127 (0 when below 2^-126, NaN when a value is not finite); the page's
+ * scale becomes the larger of t and its old scale if the page already held
+ * tokens before the call's first one, else t.  When it grows, the older tokens'
+ * codes become rint(code * (old / new)); the new codes are rint(value *
+ * (1 / scale)).  K is quantized after its rotation.  A page that a NaN scale
+ * reached reads as NaN until its first token is written again.
+ * A page in the tables of several sequences must not be appended to by two
+ * of them in one call.  Pointers of type dt: 16-byte aligned, row strides a
+ * multiple of 16 bytes.  Deterministic; asynchronous on `stream`; no scratch.
+ */
+int pq_kv_append(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt,
+                 const void *k, long long ldk, const void *v, long long ldv,
+                 const void *q, long long ldq, int n_q, void *q_out, long long ldqo,
+                 const float *rope_cos, const float *rope_sin, int n_pos, int rot, int rope_mode,
+                 struct CUstream_st *stream);
+
+/*
+ * Read cached tokens back as values of type dt, scale * code rounded once:
+ * k_out, v_out device [n_rows][n_kv * d] with row strides ldk, ldv; the rows
+ * are placed as above (the last tokens of each sequence).
+ */
+int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt,
+                 void *k_out, long long ldk, void *v_out, long long ldv, struct CUstream_st *stream);
+
+/*
+ * Causal attention over the cache:
+ *   out[r][h] = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale * (q[r][h] . k_t))
+ * over the tokens t of the row's sequence, kv head h / (n_q / n_kv), with
+ *   t <= pos   and   (window == 0  or  pos - t < window  or  t < n_sink),
+ * pos being the row's position: window counts the row's own token; the first
+ * n_sink tokens stay visible whatever the window.  A row that sees no token
+ * gives zeros.  The tokens of this call must have been appended before it.
+ *
+ *   q     device [n_rows][n_q * d] of type dt, row stride ldq (elements)
+ *   out   device [n_rows][n_q * d] of type dt, row stride ldo; overlaps
+ *         neither q nor the cache
+ *   ws    device, 16-byte aligned, at least pq_attn_ws_bytes(...) bytes, zeros
+ *         before its first use; every call leaves it ready for the next.
+ *         Calls that may overlap on the GPU need one each.
+ * Accumulation in f32; q and the softmax weights enter the tensor cores as fp16
+ * (f32 rows: as fp16 pairs), the codes exactly.  Deterministic.
+ */
+int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt,
+            const void *q, long long ldq, int n_q, float scale, int window, int n_sink,
+            void *out, long long ldo, void *ws, size_t ws_bytes, struct CUstream_st *stream);
+
+/* Workspace bytes for any pq_attn call with these head counts and head size
+ * (0 for sizes pq_attn rejects). */
+size_t pq_attn_ws_bytes(int n_q, int n_kv, int d);
 
 #ifdef __cplusplus
 }

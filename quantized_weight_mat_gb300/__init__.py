@@ -23,16 +23,31 @@ KERNELS = {"auto": KERNEL_AUTO, "generic": KERNEL_GENERIC, "stream": KERNEL_STRE
 PQ_OK = 0
 PQ_ERR_ARG, PQ_ERR_FMT, PQ_ERR_K, PQ_ERR_ALIGN = -1, -2, -3, -4
 PQ_ERR_SIZE, PQ_ERR_DEVICE, PQ_ERR_LAUNCH, PQ_ERR_KERNEL = -5, -6, -7, -8
+PQ_ERR_DTYPE, PQ_ERR_LAYOUT, PQ_ERR_WS = -9, -10, -11
+
+F32, F16, BF16 = 0, 1, 2
+DTYPES = {"f32": F32, "f16": F16, "bf16": BF16}
+ROPE_HALF, ROPE_PAIR = 0, 1
+ROPES = {"half": ROPE_HALF, "pair": ROPE_PAIR}
 
 LIB_PATH = os.environ.get("PQ_LIB_PATH") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "libpq.so")
 EXPORTS = ("pq_gemv", "pq_dequant", "pq_weight_bytes", "pq_strerror",
            "pq_gemv_kernel", "pq_gemv_choice", "pq_gemv_launches", "pq_wait_timeouts",
            "pq_set_weight_prefetch", "pq_gemv_noalloc", "pq_selftest_wait_timeout",
-           "pq_gemv_bias", "pq_gemv_swiglu")
+           "pq_gemv_bias", "pq_gemv_swiglu",
+           "pq_kv_append", "pq_kv_gather", "pq_attn", "pq_attn_ws_bytes")
 
 _lock = threading.Lock()
 _lib = None
+
+
+class KVCache(ctypes.Structure):
+    """``pq_kv_cache`` of include/pq.h; made by ``pq_kv_cache``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int), ("n_kv", ctypes.c_int), ("page", ctypes.c_int), ("d", ctypes.c_int),
+                ("n_seq", ctypes.c_int), ("table_ld", ctypes.c_int)]
 
 
 class PQError(RuntimeError):
@@ -75,6 +90,15 @@ def lib() -> ctypes.CDLL:
             L.pq_gemv_bias.restype = i32
             L.pq_gemv_swiglu.argtypes = [i32, vp, i32, i32, vp, i32, vp, vp]
             L.pq_gemv_swiglu.restype = i32
+            ll, cp = ctypes.c_longlong, ctypes.POINTER(KVCache)
+            L.pq_kv_append.argtypes = [cp, vp, i32, i32, vp, ll, vp, ll, vp, ll, i32, vp, ll, vp, vp, i32, i32, i32, vp]
+            L.pq_kv_append.restype = i32
+            L.pq_kv_gather.argtypes = [cp, vp, i32, i32, vp, ll, vp, ll, vp]
+            L.pq_kv_gather.restype = i32
+            L.pq_attn.argtypes = [cp, vp, i32, i32, vp, ll, i32, ctypes.c_float, i32, i32, vp, ll, vp, sz, vp]
+            L.pq_attn.restype = i32
+            L.pq_attn_ws_bytes.argtypes = [i32, i32, i32]
+            L.pq_attn_ws_bytes.restype = sz
             L.pq_set_weight_prefetch.argtypes = [i32]
             L.pq_set_weight_prefetch.restype = i32
             _lib = L
@@ -186,3 +210,53 @@ def pq_gemv_noalloc(fmt, w_blocks, n_out: int, k: int, x, batch: int, y, stream=
 def pq_selftest_wait_timeout(limit_us: int, stream=None) -> int:
     """Bounded-wait self-test (see include/pq.h): 1 when the wait ran out as designed."""
     return int(lib().pq_selftest_wait_timeout(int(limit_us), _stream(stream)))
+
+
+def _dtype(dt) -> int:
+    return DTYPES[dt] if isinstance(dt, str) else int(dt)
+
+
+def pq_kv_cache(k, v, k_scale, v_scale, table, len_, n_pages: int, n_kv: int, page: int, d: int, n_seq: int,
+                table_ld: int) -> KVCache:
+    """Handle on a paged 8-bit cache (see include/pq.h); keeps the buffers it is given alive."""
+    c = KVCache(_addr(k), _addr(v), _addr(k_scale), _addr(v_scale), _addr(table), _addr(len_),
+                int(n_pages), int(n_kv), int(page), int(d), int(n_seq), int(table_ld))
+    c.buffers = (k, v, k_scale, v_scale, table, len_)
+    return c
+
+
+def pq_kv_append(cache: KVCache, row_start, n_rows: int, dt, k, ldk: int, v, ldv: int, q=None, ldq: int = 0,
+                 n_q: int = 0, q_out=None, ldqo: int = 0, rope_cos=None, rope_sin=None, n_pos: int = 0, rot: int = 0,
+                 rope_mode="half", stream=None, check: bool = True) -> int:
+    """Append rotated keys and values to the cache; rotates q into q_out beside them when given."""
+    mode = ROPES[rope_mode] if isinstance(rope_mode, str) else int(rope_mode)
+    st = lib().pq_kv_append(cache, _addr(row_start), n_rows, _dtype(dt), _addr(k), ldk, _addr(v), ldv, _addr(q), ldq,
+                            n_q, _addr(q_out), ldqo, _addr(rope_cos), _addr(rope_sin), n_pos, rot, mode,
+                            _stream(stream))
+    if check and st:
+        raise PQError(st, "pq_kv_append")
+    return st
+
+
+def pq_kv_gather(cache: KVCache, row_start, n_rows: int, dt, k_out, ldk: int, v_out, ldv: int, stream=None,
+                 check: bool = True) -> int:
+    """Read the last tokens of each sequence back from the cache as values of type dt."""
+    st = lib().pq_kv_gather(cache, _addr(row_start), n_rows, _dtype(dt), _addr(k_out), ldk, _addr(v_out), ldv,
+                            _stream(stream))
+    if check and st:
+        raise PQError(st, "pq_kv_gather")
+    return st
+
+
+def pq_attn(cache: KVCache, row_start, n_rows: int, dt, q, ldq: int, n_q: int, scale: float, window: int,
+            n_sink: int, out, ldo: int, ws, ws_bytes: int, stream=None, check: bool = True) -> int:
+    """Causal attention of the rows over the cache; window 0: every token, else the last `window` and first `n_sink`."""
+    st = lib().pq_attn(cache, _addr(row_start), n_rows, _dtype(dt), _addr(q), ldq, n_q, scale, window, n_sink,
+                       _addr(out), ldo, _addr(ws), ws_bytes, _stream(stream))
+    if check and st:
+        raise PQError(st, "pq_attn")
+    return st
+
+
+def pq_attn_ws_bytes(n_q: int, n_kv: int, d: int) -> int:
+    return int(lib().pq_attn_ws_bytes(int(n_q), int(n_kv), int(d)))

@@ -267,6 +267,9 @@ const char *pq_strerror(int status) {
     case PQ_ERR_DEVICE: return "current device is not compute capability 10.3 (sm_103)";
     case PQ_ERR_LAUNCH: return "CUDA kernel launch failed";
     case PQ_ERR_KERNEL: return "the requested kernel does not support this case";
+    case PQ_ERR_DTYPE: return "unknown element type";
+    case PQ_ERR_LAYOUT: return "head size, head counts, page size or rotated size not supported";
+    case PQ_ERR_WS: return "workspace too small (pq_attn_ws_bytes)";
     }
     return "unknown status";
 }
