@@ -15,9 +15,11 @@ bool span_overlaps(const void *a, int64_t na, const void *b, int64_t nb) {
     return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
 }
 
-int check_gb300() {
+int check_gb300(const DeviceInfo **out = nullptr) {
     const DeviceInfo *dev = device_info();
-    return dev && dev->major == 10 && dev->minor == 3 ? PQ_OK : PQ_ERR_DEVICE;
+    if (!dev || dev->major != 10 || dev->minor != 3) return PQ_ERR_DEVICE;
+    if (out) *out = dev;
+    return PQ_OK;
 }
 
 constexpr int64_t kMost = INT64_C(1) << 40;
@@ -162,7 +164,7 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
 
 size_t pq_attn_ws_bytes(int n_q, int n_kv, int d) {
     if (n_q <= 0 || n_kv <= 0 || n_q % n_kv || !head_size_ok(d)) return 0;
-    return 16;
+    return d == 64 || d == 128 ? attn_mma_ws_bytes(d) : 16;
 }
 
 int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt, const void *q, long long ldq,
@@ -176,6 +178,7 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     if (n_q <= 0 || window < 0 || n_sink < 0 || !std::isfinite(scale) || !ws) return PQ_ERR_ARG;
     if (n_q % c.n_kv) return PQ_ERR_LAYOUT;
     const int64_t w = (int64_t)n_q * c.d;
+    if ((int64_t)n_rows * n_q > (INT64_C(1) << 30)) return PQ_ERR_SIZE;
     if ((st = check_rows(q, ldq, w, n_rows, eb)) || (st = check_rows(out, ldo, w, n_rows, eb))) return st;
     if ((uintptr_t)ws % 16) return PQ_ERR_ALIGN;
     if (ws_bytes < pq_attn_ws_bytes(n_q, c.n_kv, c.d)) return PQ_ERR_WS;
@@ -183,7 +186,8 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     if (span_overlaps(out, ob, q, qb) || touches_cache(out, ob, c) || span_overlaps(ws, (int64_t)ws_bytes, out, ob) ||
         span_overlaps(ws, (int64_t)ws_bytes, q, qb) || touches_cache(ws, (int64_t)ws_bytes, c))
         return PQ_ERR_ARG;
-    if ((st = check_gb300())) return st;
+    const DeviceInfo *dev = nullptr;
+    if ((st = check_gb300(&dev))) return st;
     if (n_rows == 0) return PQ_OK;
     AttnArgs a;
     a.c = view_of(c, row_start, n_rows);
@@ -193,10 +197,15 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     a.ldo = ldo;
     a.scale = scale;
     a.n_q = n_q;
-    a.window = window;
-    a.n_sink = n_sink;
+    // positions stay below 2^30 (check_cache), so larger values change nothing
+    a.window = window < (1 << 30) ? window : 1 << 30;
+    a.n_sink = n_sink < (1 << 30) ? n_sink : 1 << 30;
     a.ws = static_cast<uint8_t *>(ws);
-    return launch_attn_generic((int)dt, a, stream) == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
+    const int group = n_q / c.n_kv;
+    const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
+    const cudaError_t e = c.d == 64 || c.d == 128 ? launch_attn_mma((int)dt, a, rows, stream, *dev)
+                                                  : launch_attn_generic((int)dt, a, stream);
+    return e == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -40,6 +40,12 @@ struct AttnArgs {
 cudaError_t launch_kv_append(int dt, const KvAppendArgs &a, cudaStream_t s);
 cudaError_t launch_kv_gather(int dt, const KvView &c, void *k_out, long long ldk, void *v_out, long long ldv,
                              cudaStream_t s);
+// Attention for head sizes 64 and 128, `rows` (tokens times query heads per kv
+// head) of a typical sequence deciding between row tiles of 8 and 16 rows.
+cudaError_t launch_attn_mma(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev);
+size_t attn_mma_ws_bytes(int d);
+unsigned attn_mma_wait_timeouts(bool reset);
+// Any head size, CUDA cores.
 cudaError_t launch_attn_generic(int dt, const AttnArgs &a, cudaStream_t s);
 
 }  // namespace pqk

@@ -9,7 +9,7 @@
 #include <cstdlib>
 #include <mutex>
 
-#include "pq_internal.h"
+#include "kv_internal.h"
 
 namespace pqk {
 
@@ -343,7 +343,8 @@ int pq_wait_timeouts(int reset) {
     const DeviceInfo *dev = nullptr;
     if (check_device(&dev)) return PQ_ERR_DEVICE;
     const unsigned n =
-        stream_wait_timeouts(reset != 0) + tc_wait_timeouts(reset != 0) + selftest_wait_timeouts(reset != 0);
+        stream_wait_timeouts(reset != 0) + tc_wait_timeouts(reset != 0) + selftest_wait_timeouts(reset != 0) +
+        attn_mma_wait_timeouts(reset != 0);
     return n > 0x7fffffffu ? 0x7fffffff : (int)n;
 }
 
