@@ -12,19 +12,24 @@
 // (0x6400 | (code + 128) is 1152 + code); q is scaled per row by a power of
 // two into fp16's range (one fp16 for 16-bit rows, an fp16 pair for f32 rows).
 // The softmax weights enter in fp16 (f32 rows: an fp16 pair), already times
-// their page's V scale over the largest one seen so far: weights and ratios
-// are at most 1 times the 2^8 that the running maximum may lag behind, so fp16
-// holds them whatever the scales.
+// their page's V scale over a power of two above the largest one the row has
+// seen: ratios are at most 1 and weights at most the 2^8 that the running
+// maximum may lag behind, so fp16 holds them whatever the scales.  Both
+// references move rarely (the maximum by 2^8, the power of two at 4 to 8 times the
+// scale that set it): rescaling O costs a warp half a tile's time.
 //
 // ldmatrix gives a thread four codes of one token (K) or, transposed in 2-byte
 // units, two elements of two tokens (V): the byte permutes of the conversion
 // sort them, so the transposition of V costs nothing.
 //
-// Pipeline: warp 4 brings 64-token tiles of K and V through a ring of stages (TMA boxes
-// of one page or half a page, swizzled; page numbers read for eight tiles at a
-// time; page scales by 4-byte asynchronous copies onto the same barrier); warps
-// 0-3 take 16 tokens of a tile each, with a running maximum of their own,
-// and join at the end of an item.
+// Pipeline: warp 4 walks the CTA's units (the other warps get each item from it
+// through a small ring) and brings 128-token tiles of K and V through a ring of
+// stages (one TMA box per page, swizzled; page numbers read for four tiles at a
+// time; page scales by 4-byte asynchronous copies onto the same barrier); warp 5
+// turns the next item's rows of q into fp16 operands in shared memory while
+// the present item runs; warps 0-3 take 32 tokens of a tile each, as two independent
+// groups of 16, with a running maximum of their own, and join at the end of
+// an item.
 
 #include <cuda.h>
 
@@ -35,23 +40,34 @@
 namespace pqk {
 namespace {
 
-constexpr int KT = 64;                       // tokens per tile
-constexpr int kConsumers = 4;                // warps, 16 tokens of a tile each
-constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int KT = 128;                      // tokens per tile
+constexpr int kConsumers = 4;                // warps, 32 tokens of a tile each
+constexpr int kGroups = KT / 16;             // groups of 16 tokens: always within one page
+constexpr int kThreads = 32 * (kConsumers + 2);
+constexpr int kItemCost = 2;                 // see attn_sched.cuh
+constexpr int kItems = 8;                    // items that the walking warp may be ahead (more than the tiles it looks up at a time)
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMinExp = -200, kMaxExp = 125;   // of V scales: none seen yet, and the largest
 constexpr float kSlack = 8.f;                // the running maximum may lag by this many powers of two
 
 template <int D> __host__ __device__ constexpr int tile_bytes() { return KT * D; }
-template <int D> __host__ __device__ constexpr int stages() { return D == 128 ? 5 : 10; }
-// join buffer: 8 rows of each consumer warp at a time
-template <int D> __host__ __device__ constexpr int red_bytes() { return kConsumers * 8 * (D + 8) * 4; }
-template <int D> __host__ __device__ constexpr int smem_bytes() {
-    return 1024 + stages<D>() * 2 * tile_bytes<D>() + red_bytes<D>();
+template <int D> __host__ __device__ constexpr int stages() { return D == 128 ? 3 : 6; }
+// q as fp16: row pitch in elements (8 words past a multiple of 32 banks)
+template <int D> __host__ __device__ constexpr int q_pitch() { return D + 16; }
+template <int D> __host__ __device__ constexpr int red_pitch() { return D + 8; }
+// One buffer for q (hi rows, for f32 lo rows) while an item runs, and for the
+// join of 4 rows of each warp at its end.
+template <int D, int NT, bool PAIR> __host__ __device__ constexpr int shared_bytes() {
+    const int q = 8 * NT * (PAIR ? 2 : 1) * q_pitch<D>() * 2, red = kConsumers * 4 * red_pitch<D>() * 4;
+    return q > red ? q : red;
+}
+template <int D, int NT, bool PAIR> __host__ __device__ constexpr int smem_bytes() {
+    return 1024 + stages<D>() * 2 * tile_bytes<D>() + shared_bytes<D, NT, PAIR>();
 }
 
 struct TileMeta {
-    float ks[4], vs[4];      // scales of the tile's four groups of 16 tokens
-    int have[4];             // whether the group has a page
+    float ks[kGroups], vs[kGroups];      // scales of the tile's groups of 16 tokens
+    int have[kGroups];                   // whether the group has a page
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -59,6 +75,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^e, 0 below the smallest normal number, 2^127 above it.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(min(max(e, -127), 127) + 127) << 23); }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -73,7 +91,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -115,62 +133,161 @@ template <class T> __device__ __forceinline__ void load4(const T *p, float (&x)[
     for (int i = 0; i < 4; ++i) x[i] = to_f32(e[i]);
 }
 
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+template <class T> __device__ __forceinline__ void store4(T *p, float4 v) {
+    T e[4];
+    from_f32(e[0], v.x);
+    from_f32(e[1], v.y);
+    from_f32(e[2], v.z);
+    from_f32(e[3], v.w);
+    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(e);
+}
+
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_mma(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs p) {
     constexpr int RT = 8 * NT, NS = stages<D>(), CH = D / 16;
     constexpr bool PAIR = sizeof(T) == 4;            // q and the weights as fp16 pairs
-    constexpr float kLift = PAIR ? 128.f : 1.f;      // keeps the low halves of small weights above fp16's last bit
-    constexpr int RLD = D + 8;                       // row pitch of the join buffer
+    constexpr int kLiftExp = PAIR ? 7 : 0;           // keeps the low halves of small weights above fp16's last bit
+    constexpr int RLD = red_pitch<D>(), QP = q_pitch<D>();
+    constexpr int AHEAD_C = NT == 1 ? CH / 2 : 1;    // K chunk pairs loaded ahead of their use
+    using Walk = UnitWalk<RT, KT, kItemCost>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[NS], empty[NS];
+    __shared__ __align__(8) uint64_t full[NS], empty[NS], i_full[kItems], i_empty[kItems], q_full, q_empty;
     __shared__ __align__(16) TileMeta meta[NS];
-    __shared__ UnitRange range;
-    __shared__ float red_m[kConsumers][RT], red_l[kConsumers][RT];
+    __shared__ Item items[kItems];
+    __shared__ long long q_out[RT];
+    __shared__ float red_m[kConsumers][RT], red_l[kConsumers][RT], q_fac[RT];
+    __shared__ int q_pos[RT];
     __shared__ int last_part;
 
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *shared = ring + NS * 2 * tile_bytes<D>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = p.n_q / p.c.n_kv;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 1 + 4);
+            mbar_init(&full[i], 1 + kGroups);
             mbar_init(&empty[i], kConsumers);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&i_full[i], 1);
+            mbar_init(&i_empty[i], 2);
+        }
+        mbar_init(&q_full, 1);
+        mbar_init(&q_empty, 1);
         fence_mbar_init();
     }
-    find_range<RT, KT, kThreads>(p, group, &range);
-    const int count = (int)(range.last - range.first);
-    if (count == 0) return;
+    if (threadIdx.x == 32 * kConsumers) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+    }
+    __syncthreads();
+    // what the preceding kernels on the stream wrote (lengths, table, codes, q)
+    // is complete after this; the next kernel may then be scheduled beside this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
 
-    UnitWalk<RT, KT> at;
-    at.start(p, group, range.seq, range.offset, range.per_head);
+    if (warp == kConsumers + 1) {
+        // ---------------- rows of q ----------------
+        constexpr int LPR = D / 4, RPP = 32 / LPR, NP = RT / RPP;      // lanes per row, rows per pass, passes
+        const int sub = lane / LPR, col = lane % LPR;
+        for (uint32_t k = 0;; ++k) {
+            if (!mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) return;
+            const Item it = items[k % kItems];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&i_empty[k % kItems]);
+            if (it.n == 0) return;
+            float v[NP][4];
+            int tok[NP], head[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int r = i * RPP + sub, rr = it.j * RT + r;
+                tok[i] = p.group.div(rr);
+                head[i] = it.h * p.group.d + rr - tok[i] * p.group.d;
+                if (r < it.rows)
+                    load4(static_cast<const T *>(p.q) + (it.r0 + tok[i]) * p.ldq + (long long)head[i] * D + 4 * col, v[i]);
+                else v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+            }
+            if (!mbar_wait(&q_empty, (k + 1) & 1u)) return;
+            __half *q = reinterpret_cast<__half *>(shared);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int r = i * RPP + sub;
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7fffffffu);
+#pragma unroll
+                for (int w = LPR / 2; w > 0; w >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const int ex = tc_scale_exponent(top);
+                const float up = __uint_as_float((uint32_t)(127 + ex) << 23), down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] *= up;
+                const uint32_t h[2] = {pack2(v[i][0], v[i][1]), pack2(v[i][2], v[i][3])};
+                *reinterpret_cast<uint2 *>(q + r * QP + 4 * col) = make_uint2(h[0], h[1]);
+                if constexpr (PAIR) {
+                    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h[0]));
+                    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h[1]));
+                    *reinterpret_cast<uint2 *>(q + (RT + r) * QP + 4 * col) =
+                        make_uint2(pack2(v[i][0] - a.x, v[i][1] - a.y), pack2(v[i][2] - b.x, v[i][3] - b.y));
+                }
+                if (col == 0) {
+                    q_fac[r] = down * (p.scale * kLog2e);
+                    q_pos[r] = r < it.rows ? it.len - it.m + tok[i] : -1;
+                    q_out[r] = (it.r0 + tok[i]) * p.ldo + (long long)head[i] * D;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+        }
+        return;
+    }
 
     if (warp == kConsumers) {
         // ---------------- producer ----------------
-        const int box = min(p.c.page, KT);                     // tokens per TMA box
-        const int g = lane & 3, sub = lane >> 2;
-        for (int n0 = 0; n0 < count; n0 += 8) {
-            // lane 4i + g looks up group g of unit n0 + i
-            int tok = 0, seq = 0, head = 0;
-            for (int i = 0; i < 8 && n0 + i < count; ++i) {
-                if (sub == i) {
+        constexpr int BATCH = 32 / kGroups;                    // tiles looked up at a time
+        const int g = lane % kGroups, sub = lane / kGroups;
+        Walk at;
+        long long first, last;
+        const Cut cut = find_range<Walk, kItemCost>(p, at, first, last);
+        int slot = 0;
+        uint32_t phase = 1, k = 0;
+        bool fresh = true;
+        at.w = first == last ? last : at.w;
+        while (at.w < last) {
+            // lane kGroups * i + g looks up group g of the i-th unit from here
+            int tok = 0, seq = 0, head = 0, n = 0;
+            for (; n < BATCH && at.w < last; ++n) {
+                if (fresh) {
+                    fresh = false;
+                    if (!mbar_wait(&i_empty[k % kItems], (k / kItems + 1) & 1u)) return;
+                    if (lane == 0) {
+                        items[k % kItems] = item_of(at, cut, first, last);
+                        mbar_arrive(&i_full[k % kItems]);
+                    }
+                    ++k;
+                }
+                if (sub == n) {
                     tok = at.token0() + 16 * g;
                     seq = at.s;
                     head = at.h;
                 }
-                at.next(p, group);
+                if (at.y + 1 < at.t.units) {
+                    ++at.y;
+                    ++at.w;
+                } else {
+                    at.next_item(p);
+                    fresh = true;
+                }
             }
-            const int pg = n0 + sub < count ? page_of(p.c, seq, tok / p.c.page) : -1;
-            for (int i = 0; i < 8 && n0 + i < count; ++i) {
-                const int n = n0 + i, slot = n % NS;
-                if (!mbar_wait(&empty[slot], (uint32_t)(n / NS + 1) & 1u)) return;
+            const int pg = sub < n ? page_of(p.c, seq, tok / p.c.page) : -1;
+            for (int i = 0; i < n; ++i) {
+                if (!mbar_wait(&empty[slot], phase)) return;
                 if (sub == i) meta[slot].have[g] = pg >= 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * tile_bytes<D>());
                 __syncwarp();
                 if (sub == i) {
-                    if (16 * g % box == 0) {
+                    if (16 * g % p.c.page == 0) {
                         // no page: a box outside the tensor, which reads as zeros
                         const int row = head * p.c.page + tok % p.c.page, z = pg >= 0 ? pg : p.c.n_pages;
                         const uint32_t dst = smem_u32(ring + slot * 2 * tile_bytes<D>()) + 16 * g * D;
@@ -182,7 +299,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                     copy4(&meta[slot].vs[g], p.c.v_scale + si, pg >= 0);
                     copies_arrive(&full[slot]);
                 }
+                if (++slot == NS) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
             }
+        }
+        if (!mbar_wait(&i_empty[k % kItems], (k / kItems + 1) & 1u)) return;
+        if (lane == 0) {
+            items[k % kItems].n = 0;
+            mbar_arrive(&i_full[k % kItems]);
         }
         return;
     }
@@ -191,133 +317,185 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int g = lane >> 2, t = lane & 3;
     // ldmatrix: this lane gives the address of row lr of 16-byte chunk 2c + lc
     const int lr = (lane & 7) + 8 * ((lane >> 3) & 1), lc = lane >> 4;
-    const uint32_t lrow = (uint32_t)((16 * warp + lr) * D);
+    const uint32_t lrow = (uint32_t)((32 * warp + lr) * D);
     const uint32_t lswz = D == 128 ? (uint32_t)(lr & 7) : (uint32_t)((lr >> 1) & 3);
-    float *red = reinterpret_cast<float *>(ring + NS * 2 * tile_bytes<D>());
+    const uint32_t lofs = ((uint32_t)lc ^ lswz) << 4;      // chunk c of the row lies at lrow + ((16 c) ^ lofs)
+    float *red = reinterpret_cast<float *>(shared);
+    const __half *qrow = reinterpret_cast<const __half *>(shared) + g * QP + 4 * t;
 
-    uint32_t qh[NT][CH][2], ql[PAIR ? NT : 1][PAIR ? CH : 1][2];
+    // one block of 8 rows: q stays in registers; two: it is read where it is used
+    uint32_t qh[CH][2], ql[PAIR ? CH : 1][2];
     float fac[NT][2];                                // of rows 2t, 2t+1: undoes q's scale, times scale * log2 e
     int pos[NT][2];                                  // their positions, -1 for none
-    float m[NT][2], l[NT][2], vref[NT][2], o[NT][CH][4];
-    float vinv[NT][2];                               // kLift / vref
-    bool fresh = true, dead = false;
-    for (int n = 0; n < count; ++n) {
-        if (fresh) {
-            fresh = false;
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                // row g of this block of 8: query head and token
-                const int r = at.j * RT + 8 * x + g;
-                const bool have = 8 * x + g < at.t.rows;
-                const T *src = static_cast<const T *>(p.q) + (long long)(at.r0 + r / group) * p.ldq +
-                               (long long)(at.h * group + r % group) * D + 4 * t;
-                float v[CH][4];
-                uint32_t top = 0;
+    float m[NT][2], l[NT][2], o[NT][CH][4];
+    int vexp[NT][2];                                 // V scales are taken over 2^vexp
+    bool dead = false;
+    int slot = 0;
+    uint32_t phase = 0;
+    for (uint32_t k = 0;; ++k) {
+        if (!dead && !mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) dead = true;
+        const Item &it = items[k % kItems];
+        if (dead || it.n == 0) return;
+        const int y0 = it.y0, n = it.n, pos0 = it.pos0, pos1 = it.pos1, sinks = it.sinks, w0 = it.w0;
+        if (!mbar_wait(&q_full, k & 1u)) dead = true;
+        {
+            if constexpr (NT == 1) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    if (have) load4(src + 16 * c, v[c]);
-                    else v[c][0] = v[c][1] = v[c][2] = v[c][3] = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[c][e]) & 0x7fffffffu);
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int ex = tc_scale_exponent(top);
-                const float up = __uint_as_float((uint32_t)(127 + ex) << 23), down = __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll
-                for (int c = 0; c < CH; ++c)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float a = v[c][2 * e] * up, b = v[c][2 * e + 1] * up;
-                        qh[x][c][e] = pack2(a, b);
-                        if constexpr (PAIR) {
-                            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&qh[x][c][e]));
-                            ql[x][c][e] = pack2(a - hi.x, b - hi.y);
-                        }
+                    const uint2 h = *reinterpret_cast<const uint2 *>(qrow + 16 * c);
+                    qh[c][0] = h.x;
+                    qh[c][1] = h.y;
+                    if constexpr (PAIR) {
+                        const uint2 lo = *reinterpret_cast<const uint2 *>(qrow + RT * QP + 16 * c);
+                        ql[c][0] = lo.x;
+                        ql[c][1] = lo.y;
                     }
-                const float f = down * (p.scale * kLog2e);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    fac[x][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));
-                    const int rr = 8 * x + 2 * t + e;
-                    pos[x][e] = rr < at.t.rows ? at.len - at.m + (at.j * RT + rr) / group : -1;
+                    fac[x][e] = q_fac[8 * x + 2 * t + e];
+                    pos[x][e] = q_pos[8 * x + 2 * t + e];
                     m[x][e] = -INFINITY;
-                    l[x][e] = vref[x][e] = vinv[x][e] = 0.f;
+                    l[x][e] = 0.f;
+                    vexp[x][e] = pos[x][e] < 0 ? kMaxExp : kMinExp;      // a row without tokens takes no page's scale
                 }
 #pragma unroll
                 for (int c = 0; c < CH; ++c) o[x][c][0] = o[x][c][1] = o[x][c][2] = o[x][c][3] = 0.f;
             }
         }
-        const int slot = n % NS;
-        if (!dead && !mbar_wait(&full[slot], (uint32_t)(n / NS) & 1u)) dead = true;
-        const int t0 = at.token0() + 16 * warp;
-        const float ks = meta[slot].ks[warp], vs = meta[slot].vs[warp];
+        for (int y = y0; y < y0 + n; ++y) {
+        if (!dead && !mbar_wait(&full[slot], phase)) dead = true;
+        const int t0 = (y < sinks ? y : w0 + (y - sinks)) * KT + 32 * warp;
+        const TileMeta &mt = meta[slot];
+        // both groups: a page, and every row sees every token
+        const bool have0 = mt.have[2 * warp], have1 = mt.have[2 * warp + 1];
+        const float ks[2] = {mt.ks[2 * warp], mt.ks[2 * warp + 1]}, vs[2] = {mt.vs[2 * warp], mt.vs[2 * warp + 1]};
         // nothing to see: no page, after the last row's token, or between the sinks and the first row's window
-        const bool skip = !meta[slot].have[warp] || t0 > at.t.pos1 ||
-                          (p.window > 0 && t0 >= p.n_sink && t0 + 15 <= at.t.pos0 - p.window);
+        const bool skip = !(have0 || have1) || t0 > pos1 ||
+                          (p.window > 0 && t0 >= p.n_sink && t0 + 31 <= pos0 - p.window);
         if (!skip) {
             const uint32_t kt = smem_u32(ring + slot * 2 * tile_bytes<D>()) + lrow, vt = kt + tile_bytes<D>();
-            float s[NT][4];
+            // s[i][x][0..1]: token g of group i, rows 2t and 2t+1 of block x; s[i][x][2..3]: token g + 8.
+            // Two sums (even and odd chunks) halve the chain of dependent products.
+            float s[2][NT][4], s2[2][NT][4];
 #pragma unroll
-            for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int c = 0; c < CH; c += 2) {
-                uint32_t w[4];
-                ldsm4(kt + (((uint32_t)(c + lc) ^ lswz) << 4), w);
+                for (int x = 0; x < NT; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] ^= 0x80808080u;
+                    for (int e = 0; e < 4; ++e) s[i][x][e] = s2[i][x][e] = 0.f;
+            uint32_t w[CH / 2][2][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t a[4] = {codes2<0x4140>(w[2 * i]), codes2<0x4140>(w[2 * i + 1]), codes2<0x4342>(w[2 * i]),
-                                           codes2<0x4342>(w[2 * i + 1])};
+            for (int cb = 0; cb < CH / 2; cb += AHEAD_C) {
 #pragma unroll
-                    for (int x = 0; x < NT; ++x) {
-                        mma(s[x], a, qh[x][c + i][0], qh[x][c + i][1]);
-                        if constexpr (PAIR) mma(s[x], a, ql[x][c + i][0], ql[x][c + i][1]);
+                for (int c2 = cb; c2 < cb + AHEAD_C; ++c2)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) ldsm4(kt + 16 * i * D + ((uint32_t)(32 * c2) ^ lofs), w[c2][i]);
+#pragma unroll
+                for (int c2 = cb; c2 < cb + AHEAD_C; ++c2) {
+                    uint2 b[NT][2][PAIR ? 2 : 1];
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int z = 0; z < (PAIR ? 2 : 1); ++z) {
+                                const int c = 2 * c2 + e;
+                                if constexpr (NT > 1)
+                                    b[x][e][z] = *reinterpret_cast<const uint2 *>(qrow + (z * RT + 8 * x) * QP + 16 * c);
+                                else
+                                    b[x][e][z] = z == 0 ? make_uint2(qh[c][0], qh[c][1]) : make_uint2(ql[PAIR ? c : 0][0], ql[PAIR ? c : 0][1]);
+                            }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[c2][i][e] ^= 0x80808080u;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t lo = w[c2][i][2 * e], hi = w[c2][i][2 * e + 1];
+                            const uint32_t a[4] = {codes2<0x4140>(lo), codes2<0x4140>(hi), codes2<0x4342>(lo), codes2<0x4342>(hi)};
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                                for (int z = 0; z < (PAIR ? 2 : 1); ++z) mma(e ? s2[i][x] : s[i][x], a, b[x][e][z].x, b[x][e][z].y);
+                        }
                     }
                 }
             }
-            // s[x][0..1]: token g, rows 2t and 2t+1; s[x][2..3]: token g + 8
-            const bool all = t0 + 15 <= at.t.pos0 && (p.window == 0 || t0 > at.t.pos1 - p.window || t0 + 15 < p.n_sink);
-            const float av = fabsf(vs);
-            const bool usable = av >= 1.17549435e-38f && av < INFINITY;     // else 0, or NaN in every weight
-            bool hide[NT][4];
+            // V's codes on their way while the weights are formed
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int c2 = 0; c2 < CH / 2; ++c2)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) ldsm4t(vt + 16 * i * D + ((uint32_t)(32 * c2) ^ lofs), w[c2][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][x][e] = (s[i][x][e] + s2[i][x][e]) * (ks[i] * fac[x][e & 1]);
+            const bool all = have0 && have1 && t0 + 31 <= pos0 &&
+                             (p.window == 0 || t0 > pos1 - p.window || t0 + 31 < p.n_sink);
+            uint32_t hidden = 0;                     // bit 4 (2x + i) + e: s[i][x][e] is not seen
+            if (!all) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int tok = t0 + 16 * i + g + 8 * (e >> 1), ps = pos[x][e & 1];
+                            if (tok > ps || (p.window > 0 && ps - tok >= p.window && tok >= p.n_sink) || !(i ? have1 : have0)) {
+                                hidden |= 1u << (4 * (2 * x + i) + e);
+                                s[i][x][e] = -INFINITY;
+                            }
+                        }
+            }
+            // exponents e of the V scales, |scale| < 2^e; scales below 2^-126 count as 0, and those whose codes
+            // overflow f32, infinities and NaNs make NaN of every weight
+            int ve[2];
+            float vu[2];
             bool raise = false;
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
+            for (int i = 0; i < 2; ++i) {
+                const int be = (int)(__float_as_uint(vs[i]) >> 23) & 255;
+                ve[i] = be == 0 || be > 127 + kMaxExp - 4 ? kMinExp : be - 126;
+                vu[i] = be == 0 ? 0.f : be > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs[i];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[x][e] *= ks * fac[x][e & 1];
-                    hide[x][e] = false;
-                    if (!all) {
-                        const int tok = t0 + g + 8 * (e >> 1), ps = pos[x][e & 1];
-                        hide[x][e] = tok > ps || (p.window > 0 && ps - tok >= p.window && tok >= p.n_sink);
-                        if (hide[x][e]) s[x][e] = -INFINITY;
-                    }
-                    raise |= s[x][e] > m[x][e & 1] + kSlack;
+                for (int x = 0; x < NT; ++x) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) raise |= s[i][x][e] > m[x][e & 1] + kSlack;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) raise |= ve[i] > vexp[x][e];
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) raise |= usable && av > vref[x][e];
             }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(s[x][e], s[x][e + 2]);
+                        float top = fmaxf(fmaxf(s[0][x][e], s[0][x][e + 2]), fmaxf(s[1][x][e], s[1][x][e + 2]));
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
                         const float mn = fmaxf(m[x][e], top);
                         float a = m[x][e] == -INFINITY ? 0.f : ex2(m[x][e] - mn);
                         m[x][e] = mn;
                         l[x][e] *= a;
-                        // a row takes the page's V scale only if it sees a token of the page
-                        const int ps = pos[x][e];
-                        const bool sees = t0 <= ps && !(p.window > 0 && t0 >= p.n_sink && t0 + 15 <= ps - p.window);
-                        if (sees && usable && av > vref[x][e]) {
-                            a *= vref[x][e] / av;
-                            vref[x][e] = av;
-                            vinv[x][e] = kLift / av;
+                        // a row takes a page's V scale only if it sees a token of the page
+                        int big = kMinExp;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int b = t0 + 16 * i, ps = pos[x][e];
+                            if (b <= ps && !(p.window > 0 && b >= p.n_sink && b + 15 <= ps - p.window)) big = max(big, ve[i]);
+                        }
+                        if (big > vexp[x][e]) {
+                            big += 2;                // room to grow
+                            a = vexp[x][e] == kMinExp ? 0.f : a * pow2(vexp[x][e] - big);
+                            vexp[x][e] = big;
                         }
 #pragma unroll
                         for (int c = 0; c < CH; ++c) {
@@ -326,58 +504,91 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
             }
-            const float vu = usable ? vs : (av < INFINITY ? 0.f : __int_as_float(0x7fc00000));
-            uint32_t ph[NT][2], pl[PAIR ? NT : 1][2];
+            float vinv[NT][2];
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                float w[4];
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float pr = hide[x][e] ? 0.f : ex2(s[x][e] - m[x][e & 1]);
-                    l[x][e & 1] += pr;
-                    w[e] = hide[x][e] ? 0.f : pr * (vu * vinv[x][e & 1]);
-                }
+                for (int e = 0; e < 2; ++e) vinv[x][e] = pow2(kLiftExp - vexp[x][e]);
+            uint32_t ph[2][NT][2], pl[2][PAIR ? NT : 1][2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t hi = pack2(w[2 * e], w[2 * e + 1]);
-                    ph[x][e] = transpose8x8(hi);
-                    if constexpr (PAIR) {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                        pl[x][e] = transpose8x8(pack2(w[2 * e] - f.x, w[2 * e + 1] - f.y));
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    float w[4];
+                    if (all) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            w[e] = ex2(s[i][x][e] - m[x][e & 1]);
+                            l[x][e & 1] += w[e];
+                            w[e] *= vu[i] * vinv[x][e & 1];
+                        }
+                    } else {
+                        // zeros before the sum (a row without tokens has inf - inf here) and after the scale (a
+                        // page that is not seen may have a NaN there)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const bool see = !(hidden & (1u << (4 * (2 * x + i) + e)));
+                            w[e] = see ? ex2(s[i][x][e] - m[x][e & 1]) : 0.f;
+                            l[x][e & 1] += w[e];
+                            w[e] = see ? w[e] * (vu[i] * vinv[x][e & 1]) : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t hi = pack2(w[2 * e], w[2 * e + 1]);
+                        ph[i][x][e] = transpose8x8(hi);
+                        if constexpr (PAIR) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                            pl[i][x][e] = transpose8x8(pack2(w[2 * e] - f.x, w[2 * e + 1] - f.y));
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int c = 0; c < CH; c += 2) {
-                uint32_t w[4];
-                ldsm4t(vt + (((uint32_t)(c + lc) ^ lswz) << 4), w);
+            for (int c2 = 0; c2 < CH / 2; ++c2) {
+                if constexpr (NT > 1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] ^= 0x80808080u;
+                    for (int i = 0; i < 2; ++i) ldsm4t(vt + 16 * i * D + ((uint32_t)(32 * c2) ^ lofs), w[c2][i]);
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    // row g of the fragment is element 2g of the chunk, row g + 8 element 2g + 1
-                    const uint32_t a[4] = {codes2<0x4240>(w[2 * i]), codes2<0x4341>(w[2 * i]), codes2<0x4240>(w[2 * i + 1]),
-                                           codes2<0x4341>(w[2 * i + 1])};
 #pragma unroll
-                    for (int x = 0; x < NT; ++x) {
-                        mma(o[x][c + i], a, ph[x][0], ph[x][1]);
-                        if constexpr (PAIR) mma(o[x][c + i], a, pl[x][0], pl[x][1]);
+                    for (int e = 0; e < 4; ++e) w[c2][i][e] ^= 0x80808080u;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // row g of the fragment is element 2g of the chunk, row g + 8 element 2g + 1
+                        const uint32_t lo = w[c2][i][2 * e], hi = w[c2][i][2 * e + 1];
+                        const uint32_t a[4] = {codes2<0x4240>(lo), codes2<0x4341>(lo), codes2<0x4240>(hi), codes2<0x4341>(hi)};
+#pragma unroll
+                        for (int x = 0; x < NT; ++x) {
+                            mma(o[x][2 * c2 + e], a, ph[i][x][0], ph[i][x][1]);
+                            if constexpr (PAIR) mma(o[x][2 * c2 + e], a, pl[i][x][0], pl[i][x][1]);
+                        }
                     }
                 }
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
+        if (++slot == NS) {
+            slot = 0;
+            phase ^= 1u;
+        }
+        }
 
-        const long long u = range.first + n, item0 = u - at.y, item1 = item0 + at.t.units;
-        const bool end = u + 1 == item1;
-        if (end || n + 1 == count) {
-            // ---------------- join the four warps ----------------
-            const bool whole = item0 >= range.first && item1 <= range.last;
-            const int tid = threadIdx.x;
-            const int side = item0 <= range.first ? 0 : 1;
-            float *part = reinterpret_cast<float *>(p.ws + attn_counter_bytes()) +
-                          (size_t)(2 * blockIdx.x + side) * attn_part_floats(RT, D);
+        // ---------------- the item's end: join the four warps ----------------
+        {
+            const bool whole = it.c0 == it.c1;
+            const int tid = threadIdx.x, rows = it.rows;
+            constexpr int COLS = D / 4;                      // groups of 4 elements
+            const int col = tid % COLS, line = tid / COLS;
+            float *parts = reinterpret_cast<float *>(p.ws + attn_counter_bytes());
+            constexpr size_t PF = attn_part_floats(RT, D);
+            float *part = parts + (size_t)it.slot * PF;
+            // 4 elements of a row of the item
+            auto put = [&](int row, float4 v, float sum) {
+                const float inv = sum != 0.f ? 1.f / sum : 0.f;      // no visible token: zeros
+                store4(static_cast<T *>(p.out) + q_out[row] + 4 * col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+            };
 #pragma unroll
             for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -390,49 +601,56 @@ __global__ void __launch_bounds__(kThreads, 2)
                         red_l[warp][8 * x + 2 * t + e] = sum;
                     }
                 }
+            named_sync(1, 32 * kConsumers);                  // every warp is done with q, which the buffer held
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                // 8 rows at a time through the join buffer
-                const float back[2] = {vref[x][0] * (1.f / kLift), vref[x][1] * (1.f / kLift)};
-                float *mine = red + (size_t)(warp * 8) * RLD;
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int first = 8 * x + 4 * hf;        // rows first .. first + 3
+                    if (first >= rows) continue;
+                    if ((t >> 1) == hf) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float2 *>(mine + (2 * t + e) * RLD + 16 * c + 2 * g) =
-                            make_float2(o[x][c][e] * back[e], o[x][c][e + 2] * back[e]);
-                named_sync(1, 32 * kConsumers);
-                for (int i = tid; i < 8 * D; i += 32 * kConsumers) {
-                    const int r = i / D, d = i % D, row = 8 * x + r;
-                    if (row >= at.t.rows) continue;
-                    float top = red_m[0][row];
+                        for (int e = 0; e < 2; ++e) {
+                            const float back = vexp[x][e] == kMinExp ? 0.f : pow2(vexp[x][e] - kLiftExp);
+                            float *mine = red + (warp * 4 + 2 * (t & 1) + e) * RLD + 2 * g;
 #pragma unroll
-                    for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, red_m[w][row]);
-                    float sum = 0.f, acc = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kConsumers; ++w) {
-                        const float a = red_m[w][row] == -INFINITY ? 0.f : ex2(red_m[w][row] - top);
-                        sum += red_l[w][row] * a;
-                        acc += red[(size_t)(w * 8 + r) * RLD + d] * a;
-                    }
-                    if (whole) {
-                        const int rr = at.j * RT + row;
-                        T *dst = static_cast<T *>(p.out) + (long long)(at.r0 + rr / group) * p.ldo +
-                                 (long long)(at.h * group + rr % group) * D;
-                        from_f32(dst[d], sum != 0.f ? acc / sum : 0.f);
-                    } else {
-                        part[(size_t)row * D + d] = acc;
-                        if (d == 0) {
-                            part[(size_t)RT * D + row] = top;
-                            part[(size_t)RT * D + RT + row] = sum;
+                            for (int c = 0; c < CH; ++c)
+                                *reinterpret_cast<float2 *>(mine + 16 * c) =
+                                    make_float2(o[x][c][e] * back, o[x][c][e + 2] * back);
                         }
                     }
+                    named_sync(1, 32 * kConsumers);
+                    const int row = first + line;
+                    if (line < 4 && row < rows) {
+                        float top = red_m[0][row];
+#pragma unroll
+                        for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, red_m[w][row]);
+                        float sum = 0.f;
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int w = 0; w < kConsumers; ++w) {
+                            const float a = red_m[w][row] == -INFINITY ? 0.f : ex2(red_m[w][row] - top);
+                            const float4 v = *reinterpret_cast<const float4 *>(red + (w * 4 + line) * RLD + 4 * col);
+                            sum += red_l[w][row] * a;
+                            acc.x += v.x * a;
+                            acc.y += v.y * a;
+                            acc.z += v.z * a;
+                            acc.w += v.w * a;
+                        }
+                        if (whole) {
+                            put(row, acc, sum);
+                        } else {
+                            *reinterpret_cast<float4 *>(part + row * D + 4 * col) = acc;
+                            if (col == 0) {
+                                *reinterpret_cast<float2 *>(part + RT * D + 2 * row) = make_float2(top, sum);
+                            }
+                        }
+                    }
+                    named_sync(1, 32 * kConsumers);
                 }
-                named_sync(1, 32 * kConsumers);
-            }
             if (!whole) {
                 // ---------------- join the CTAs' parts ----------------
-                const int c0 = range_owner(item0, range.total, range.grid), c1 = range_owner(item1 - 1, range.total, range.grid);
+                const int c0 = it.c0, c1 = it.c1;
                 unsigned *counter = reinterpret_cast<unsigned *>(p.ws) + c0;
                 __threadfence();
                 named_sync(1, 32 * kConsumers);
@@ -444,36 +662,52 @@ __global__ void __launch_bounds__(kThreads, 2)
                 named_sync(1, 32 * kConsumers);
                 if (last_part) {
                     __threadfence();
-                    const float *parts = reinterpret_cast<const float *>(p.ws + attn_counter_bytes());
-                    const size_t pf = attn_part_floats(RT, D);
-                    // only the first CTA's part can be the item its range ends in
-                    const int side0 = item0 <= range_begin(c0, range.total, range.grid) ? 0 : 1;
-                    const int rows = at.t.rows;
-                    for (int i = tid; i < rows * D; i += 32 * kConsumers) {
-                        const int row = i / D, d = i % D;
-                        float top = -INFINITY, sum = 0.f, acc = 0.f;
-                        for (int c = c0; c <= c1; ++c) {
-                            const float *pp = parts + (size_t)(2 * c + (c == c0 ? side0 : 0)) * pf;
-                            const float pm = __ldcg(pp + (size_t)RT * D + row);
-                            const float plv = __ldcg(pp + (size_t)RT * D + RT + row);
-                            const float pa = __ldcg(pp + (size_t)row * D + d);
-                            const float mn = fmaxf(top, pm);
-                            const float a = top == -INFINITY ? 0.f : ex2(top - mn), b = pm == -INFINITY ? 0.f : ex2(pm - mn);
-                            sum = sum * a + plv * b;
-                            acc = acc * a + pa * b;
+                    auto part_of = [&](int c) { return parts + (size_t)(2 * c + (c == c0 ? 1 : 0)) * PF; };
+                    // a line of threads per row, 4 elements a thread; the loads of 16 parts are in flight together
+                    constexpr int LINES = 32 * kConsumers / COLS, AHEAD = 16;
+                    for (int row = line; row < rows; row += LINES) {
+                        float top = -INFINITY, sum = 0.f;
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int c = c0; c <= c1; c += AHEAD) {
+                            float2 ml[AHEAD];
+                            float4 v[AHEAD];
+#pragma unroll
+                            for (int i = 0; i < AHEAD; ++i) {
+                                const float *pp = part_of(min(c + i, c1));
+                                ml[i] = __ldcg(reinterpret_cast<const float2 *>(pp + RT * D) + row);
+                                v[i] = __ldcg(reinterpret_cast<const float4 *>(pp + row * D) + col);
+                            }
+                            float mn = top;
+#pragma unroll
+                            for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, ml[i].x);
+                            const float a = top == -INFINITY ? 0.f : ex2(top - mn);
                             top = mn;
+                            sum *= a;
+                            acc.x *= a;
+                            acc.y *= a;
+                            acc.z *= a;
+                            acc.w *= a;
+#pragma unroll
+                            for (int i = 0; i < AHEAD; ++i) {
+                                const float f = c + i > c1 || ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - top);
+                                if (c + i > c1) continue;
+                                sum += ml[i].y * f;
+                                acc.x += v[i].x * f;
+                                acc.y += v[i].y * f;
+                                acc.z += v[i].z * f;
+                                acc.w += v[i].w * f;
+                            }
                         }
-                        const int rr = at.j * RT + row;
-                        T *dst = static_cast<T *>(p.out) + (long long)(at.r0 + rr / group) * p.ldo +
-                                 (long long)(at.h * group + rr % group) * D;
-                        from_f32(dst[d], sum != 0.f ? acc / sum : 0.f);
+                        put(row, acc, sum);
                     }
                 }
-                named_sync(1, 32 * kConsumers);
             }
-            fresh = true;
+            named_sync(1, 32 * kConsumers);                  // the item and the buffer are free
+            if (tid == 0) {
+                mbar_arrive(&q_empty);
+                mbar_arrive(&i_empty[k % kItems]);
+            }
         }
-        at.next(p, group);
     }
 }
 
@@ -502,7 +736,7 @@ bool make_map(CUtensorMap *map, const int8_t *codes, const KvView &c) {
     const cuuint64_t rows = (cuuint64_t)c.n_kv * c.page;
     const cuuint64_t dims[3] = {(cuuint64_t)c.d, rows, (cuuint64_t)c.n_pages};
     const cuuint64_t strides[2] = {(cuuint64_t)c.d, rows * c.d};
-    const cuuint32_t box[3] = {(cuuint32_t)c.d, (cuuint32_t)(c.page < KT ? c.page : KT), 1};
+    const cuuint32_t box[3] = {(cuuint32_t)c.d, (cuuint32_t)c.page, 1};
     const cuuint32_t es[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t *>(codes), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -510,7 +744,7 @@ bool make_map(CUtensorMap *map, const int8_t *codes, const KvView &c) {
 }
 
 template <class T, int D, int NT> cudaError_t launch(const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {
-    constexpr int smem = smem_bytes<D>();
+    constexpr int smem = smem_bytes<D, NT, sizeof(T) == 4>();
     static PerDeviceOnce once;
     cudaError_t e = once.run([] {
         return cudaFuncSetAttribute(attn_mma<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -524,8 +758,17 @@ template <class T, int D, int NT> cudaError_t launch(const AttnArgs &a, cudaStre
     long long grid = 2 * dev.sm_count;
     if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
     if (row_tiles < grid && tiles * row_tiles * a.c.n_kv < grid) grid = tiles * row_tiles * a.c.n_kv;
-    attn_mma<T, D, NT><<<(unsigned)grid, kThreads, smem, s>>>(km, vm, a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_mma<T, D, NT>, km, vm, a);
 }
 
 template <class T> cudaError_t launch_t(const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {

@@ -5,11 +5,12 @@
 // heads of that kv head, token-major) are cut into row tiles of RT rows; the
 // tokens that a row tile sees into tiles of KT tokens.  A unit is one token
 // tile of one row tile and kv head; the units of an item (sequence, kv head,
-// row tile) are consecutive.  All units, in the order sequence, kv head, row
-// tile, token tile, are cut into one contiguous equal range per CTA, so that
-// long and short sequences load every CTA alike; an item cut by a range's end
-// is joined from its CTAs' parts, in CTA order, by whichever of them is the
-// last to finish.
+// row tile) are consecutive.  Places count 1 for every unit and COST for
+// every item before its first one (what its rows' loads and the join cost, in units).  All
+// places, in the order sequence, kv head, row tile, token tile, are cut into
+// one contiguous equal range per CTA, so that long and short sequences load every CTA
+// alike; an item cut by a range's end is joined from its CTAs' parts, in CTA
+// order, by whichever of them is the last to finish.
 #pragma once
 
 #include "kv_device.cuh"
@@ -26,13 +27,12 @@ struct RowTile {
     int units;           // at least 1, so that rows that see nothing are written
 };
 
-template <int RT, int KT>
-__device__ __forceinline__ RowTile row_tile(const AttnArgs &p, int m, int len, int j, int group) {
+template <int RT, int KT> __device__ __forceinline__ RowTile row_tile(const AttnArgs &p, int m, int len, int j) {
     RowTile t;
     const int first = j * RT;
-    t.rows = min(RT, m * group - first);
-    t.pos0 = len - m + first / group;
-    t.pos1 = len - m + (first + t.rows - 1) / group;
+    t.rows = min(RT, m * p.group.d - first);
+    t.pos0 = len - m + p.group.div(first);
+    t.pos1 = len - m + p.group.div(first + t.rows - 1);
     const int cap = p.c.table_ld * p.c.page;
     const int end = t.pos1 < 0 ? 0 : min(t.pos1, cap - 1) / KT + 1;          // token tiles up to the last row's
     const int from = p.window > 0 ? max(0, t.pos0 - p.window + 1) / KT : 0;   // first tile of the first row's window
@@ -42,130 +42,179 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs &p, int m, int len, i
     return t;
 }
 
-// Where a CTA is in its range.  Every role of the CTA walks its own copy.
-template <int RT, int KT> struct UnitWalk {
+// 64-bit quotients are slow; nearly every call's numbers fit 32 bits.
+__device__ __forceinline__ long long div_places(long long a, long long b) {
+    return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+// The cut of all places into ranges: the first `longer` ranges have size + 1
+// places, the others size.
+struct Cut {
+    long long total, size, longer;
+    int grid;                         // ranges: CTAs that have work
+
+    // At most `most` ranges, each with at least one unit.
+    __device__ __forceinline__ Cut(long long total_, int most, int cost) : total(total_) {
+        grid = (int)min((long long)most, max(div_places(total, cost + 1), 1ll));
+        size = div_places(total, grid);
+        longer = total - size * grid;
+    }
+    __device__ __forceinline__ long long begin(int c) const { return c * size + min((long long)c, longer); }
+    __device__ __forceinline__ int owner(long long w) const {
+        const long long mid = longer * (size + 1);
+        return (int)(w < mid ? div_places(w, size + 1) : longer + div_places(w - mid, size));
+    }
+};
+
+// Where a CTA is in its range.
+template <int RT, int KT, int COST> struct UnitWalk {
+    long long w;             // place of the unit
     int s, h, j, y;          // sequence, kv head, row tile, unit of the row tile
     int r0, m, len, tiles;   // of the sequence: first row, tokens, length, row tiles
     RowTile t;
 
-    __device__ __forceinline__ void seq(const AttnArgs &p, int group) {
+    __device__ __forceinline__ void seq(const AttnArgs &p) {
         seq_rows(p.c, s, r0, m);
         len = seq_len(p.c, s);
-        tiles = (m * group + RT - 1) / RT;
+        tiles = (m * p.group.d + RT - 1) / RT;
     }
-    // Enter sequence `seq_` at unit x of it, `per_head` units per kv head.
-    __device__ __forceinline__ void start(const AttnArgs &p, int group, int seq_, long long x, long long per_head) {
-        s = seq_;
-        seq(p, group);
-        h = (int)(x / per_head);
-        long long left = x % per_head;
+    // Places of one kv head of the sequence.
+    __device__ __forceinline__ long long places(const AttnArgs &p) const {
+        long long n = 0;
+        for (int i = 0; i < tiles; ++i) n += row_tile<RT, KT>(p, m, len, i).units + COST;
+        return n;
+    }
+    // The first unit at place `first` or after it, which lies `x` into the
+    // sequence, of `per_head` places per kv head.
+    __device__ __forceinline__ void start(const AttnArgs &p, long long first, long long x, long long per_head) {
+        h = (int)div_places(x, per_head);
+        long long left = x - h * per_head;
         for (j = 0;; ++j) {
-            t = row_tile<RT, KT>(p, m, len, j, group);
-            if (left < t.units) break;
-            left -= t.units;
+            t = row_tile<RT, KT>(p, m, len, j);
+            if (left < t.units + COST) break;
+            left -= t.units + COST;
         }
-        y = (int)left;
+        y = max(0, (int)left - COST);
+        w = first + y + COST - left;
     }
     __device__ __forceinline__ int token0() const { return (y < t.sinks ? y : t.w0 + (y - t.sinks)) * KT; }
-    // The next unit; returns whether it belongs to another item.
-    __device__ __forceinline__ bool next(const AttnArgs &p, int group) {
-        if (++y < t.units) return false;
+    // To the first unit of the next item.
+    __device__ __forceinline__ void next_item(const AttnArgs &p) {
+        w += t.units - y + COST;
         y = 0;
         if (++j == tiles) {
             j = 0;
             if (++h == p.c.n_kv) {
                 h = 0;
                 do {
-                    if (++s >= p.c.n_seq) return true;      // past the end: no further unit is taken
-                    seq(p, group);
+                    if (++s >= p.c.n_seq) return;      // past the end: w is past every range
+                    seq(p);
                 } while (m == 0);
             }
         }
-        t = row_tile<RT, KT>(p, m, len, j, group);
-        return true;
+        t = row_tile<RT, KT>(p, m, len, j);
     }
 };
 
-// The CTA's range of units and where it starts.
-struct UnitRange {
-    long long total, first, last;     // units of the call; [first, last) is this CTA's
-    long long offset, per_head;       // in sequence seq: first unit's index, units per kv head
-    int grid;                         // CTAs that have units
-    int seq;
-};
-
-__device__ __forceinline__ long long range_begin(long long c, long long total, int grid) { return c * total / grid; }
-__device__ __forceinline__ int range_owner(long long u, long long total, int grid) { return (int)(((u + 1) * grid - 1) / total); }
-
-// Units of one kv head of sequence s.
-template <int RT, int KT> __device__ __forceinline__ long long seq_units(const AttnArgs &p, int s, int group) {
-    int r0, m;
-    seq_rows(p.c, s, r0, m);
-    if (m == 0) return 0;
-    const int len = seq_len(p.c, s), tiles = (m * group + RT - 1) / RT;
-    long long n = 0;
-    for (int j = 0; j < tiles; ++j) n += row_tile<RT, KT>(p, m, len, j, group).units;
-    return n;
+// Places of the whole call, by one warp; lane 0's `walk` of every group of 32
+// sequences is not kept.
+template <class Walk> __device__ __forceinline__ long long warp_places(const AttnArgs &p, int s, Walk &walk, int lane) {
+    walk.s = s + lane;
+    walk.m = 0;
+    if (walk.s < p.c.n_seq) walk.seq(p);
+    return walk.m > 0 ? walk.places(p) : 0;
 }
 
-// Finds the range of CTA blockIdx.x, by all NT threads of the block; the
-// answer lies in shared memory (`out`).  Ends with a barrier.
-template <int RT, int KT, int NT> __device__ __forceinline__ void find_range(const AttnArgs &p, int group, UnitRange *out) {
-    __shared__ long long warp_sum[NT / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n_seq = p.c.n_seq;
-    long long total = 0, first = 0, before = 0;
-    int grid = 1;
-    // with more sequences than threads a first pass adds the units up
-    for (int pass = n_seq > NT ? 0 : 1; pass < 2; ++pass) {
-        before = 0;
-        for (int s0 = 0; s0 < n_seq; s0 += NT) {
-            const long long mine = s0 + tid < n_seq ? seq_units<RT, KT>(p, s0 + tid, group) : 0;
-            long long incl = mine;
-#pragma unroll
+// By one warp: the places of the call, and `walk` at the first unit of CTA
+// blockIdx.x's range [first, last); first == last when it has none.
+template <class Walk, int COST>
+__device__ __forceinline__ Cut find_range(const AttnArgs &p, Walk &walk, long long &first, long long &last) {
+    const int lane = threadIdx.x & 31, n_seq = p.c.n_seq;
+    long long total = 0, incl = 0, mine = 0;
+    for (int s = 0; s < n_seq; s += 32) {
+        mine = warp_places(p, s, walk, lane);
+        incl = mine;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        incl += total;
+        total = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const Cut cut(total * p.c.n_kv, (int)gridDim.x, COST);
+    first = last = 0;
+    if (total == 0 || (int)blockIdx.x >= cut.grid) return cut;
+    first = cut.begin(blockIdx.x);
+    last = cut.begin(blockIdx.x + 1);
+    long long before = 0;
+    for (int s = 0;; s += 32) {
+        if (n_seq > 32) {      // else the first loop's one group is still there
+            mine = warp_places(p, s, walk, lane);
+            incl = mine;
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const long long up = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += up;
             }
-            __syncthreads();
-            if (lane == 31) warp_sum[warp] = incl;
-            __syncthreads();
-            long long add = before, all = 0;
-#pragma unroll
-            for (int w = 0; w < NT / 32; ++w) {
-                if (w < warp) add += warp_sum[w];
-                all += warp_sum[w];
-            }
-            incl += add;
-            before += all;
-            if (pass == 0) continue;
-            if (n_seq <= NT) total = before * p.c.n_kv;
-            grid = (int)min((long long)gridDim.x, max(total, 1ll));
-            first = range_begin(blockIdx.x, total, grid);
-            const long long lo = (incl - mine) * p.c.n_kv, hi = incl * p.c.n_kv;
-            if ((int)blockIdx.x < grid && first >= lo && first < hi) {
-                out->seq = s0 + tid;
-                out->offset = first - lo;
-                out->per_head = mine;
-            }
+            incl += before;
         }
-        if (pass == 0) total = before * p.c.n_kv;
+        const long long lo = (incl - mine) * p.c.n_kv;
+        const unsigned hit = __ballot_sync(0xffffffffu, first >= lo && first < incl * p.c.n_kv);
+        if (hit) {
+            const int src = __ffs((int)hit) - 1;
+            walk.s = __shfl_sync(0xffffffffu, walk.s, src);
+            walk.r0 = __shfl_sync(0xffffffffu, walk.r0, src);
+            walk.m = __shfl_sync(0xffffffffu, walk.m, src);
+            walk.len = __shfl_sync(0xffffffffu, walk.len, src);
+            walk.tiles = __shfl_sync(0xffffffffu, walk.tiles, src);
+            walk.start(p, first, first - __shfl_sync(0xffffffffu, lo, src), __shfl_sync(0xffffffffu, mine, src));
+            return cut;
+        }
+        before = __shfl_sync(0xffffffffu, incl, 31);
+        if (s + 32 >= n_seq) break;
     }
-    if (tid == 0) {
-        out->total = total;
-        out->grid = grid;
-        const bool any = total > 0 && (int)blockIdx.x < grid;
-        out->first = any ? first : 0;
-        out->last = any ? range_begin(blockIdx.x + 1, total, grid) : 0;
-    }
-    __syncthreads();
+    first = last = 0;
+    return cut;
+}
+
+// One item of a CTA, as its walking warp hands it to the others.
+struct Item {
+    int r0, m, len, j, h;      // see UnitWalk
+    int y0, n;                 // its units of this CTA: y0 .. y0 + n - 1; n == 0: no more items
+    int rows, pos0, pos1, sinks, w0;
+    int c0, c1;                // CTAs that share it; c0 == c1: this one alone
+    int slot;                  // its part's place in the workspace
+};
+
+template <class Walk>
+__device__ __forceinline__ Item item_of(const Walk &at, const Cut &cut, long long first, long long last) {
+    Item it;
+    it.r0 = at.r0;
+    it.m = at.m;
+    it.len = at.len;
+    it.j = at.j;
+    it.h = at.h;
+    it.y0 = at.y;
+    it.rows = at.t.rows;
+    it.pos0 = at.t.pos0;
+    it.pos1 = at.t.pos1;
+    it.sinks = at.t.sinks;
+    it.w0 = at.t.w0;
+    it.n = (int)min((long long)(at.t.units - at.y), last - at.w);
+    const long long w0 = at.w - at.y, w1 = w0 + at.t.units - 1;      // places of its first and last unit
+    it.c0 = it.c1 = (int)blockIdx.x;
+    if (w0 < first) it.c0 = cut.owner(w0);
+    if (w1 >= last) it.c1 = cut.owner(w1);
+    it.slot = 2 * (int)blockIdx.x + (w0 < first ? 0 : 1);
+    return it;
 }
 
 // Workspace: counters of the items that several CTAs share (item counter =
 // index of its first CTA; zero between calls), then two parts per CTA (slot 2c:
-// the item its range starts in, 2c + 1: the one it ends in).  A part is RT x D
-// f32 sums, then RT maxima and RT weight sums.
+// an item that began in an earlier CTA, 2c + 1: one that begins here and goes
+// on).  A part is RT x D f32 sums, then RT pairs of a maximum and a weight sum.
 __host__ __device__ constexpr size_t attn_counter_bytes() { return (size_t)kAttnMaxGrid * 4; }
-__host__ __device__ constexpr size_t attn_part_floats(int rt, int d) { return (size_t)rt * (d + 2); }
+__host__ __device__ constexpr size_t attn_part_floats(int rt, int d) { return (size_t)rt * (d + 2); }   // a multiple of 4 (rt is one of 8)
 
 }  // namespace pqk

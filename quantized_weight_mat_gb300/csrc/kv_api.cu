@@ -191,6 +191,7 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     if (n_rows == 0) return PQ_OK;
     AttnArgs a;
     a.c = view_of(c, row_start, n_rows);
+    a.group = FastDiv(n_q / c.n_kv);
     a.q = q;
     a.out = out;
     a.ldq = ldq;
@@ -201,7 +202,7 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     a.window = window < (1 << 30) ? window : 1 << 30;
     a.n_sink = n_sink < (1 << 30) ? n_sink : 1 << 30;
     a.ws = static_cast<uint8_t *>(ws);
-    const int group = n_q / c.n_kv;
+    const int group = a.group.d;
     const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
     const cudaError_t e = c.d == 64 || c.d == 128 ? launch_attn_mma((int)dt, a, rows, stream, *dev)
                                                   : launch_attn_generic((int)dt, a, stream);

@@ -26,8 +26,24 @@ struct KvAppendArgs {
     int n_q, n_pos, rot, pair;   // pair: rotate (2i, 2i+1) instead of (i, i + rot/2)
 };
 
+// Quotients by a divisor known on the host, exact for 0 <= n < 2^31:
+// n / d = (mulhi(n, magic) + n) >> shift with shift = ceil(log2 d) and magic =
+// floor(2^32 (2^shift - d) / d) + 1 (Granlund and Montgomery, 1994).
+struct FastDiv {
+    unsigned magic, shift;
+    int d;
+    explicit FastDiv(int divisor = 1) : shift(0), d(divisor) {
+        while ((1u << shift) < (unsigned)d) ++shift;
+        magic = (unsigned)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((unsigned)n, magic) + (unsigned)n) >> shift); }
+#endif
+};
+
 struct AttnArgs {
     KvView c;
+    FastDiv group;             // query heads per kv head
     const void *q;
     void *out;
     long long ldq, ldo;
