@@ -31,24 +31,15 @@
 // groups of 16, with a running maximum of their own, and join at the end of
 // an item.
 
-#include <cuda.h>
-
-#include "attn_sched.cuh"
-#include "pq_device.cuh"
-#include "pq_ptx.cuh"
+#include "attn_common.cuh"
 
 namespace pqk {
 namespace {
 
-constexpr int KT = 128;                      // tokens per tile
 constexpr int kConsumers = 4;                // warps, 32 tokens of a tile each
-constexpr int kGroups = KT / 16;             // groups of 16 tokens: always within one page
 constexpr int kThreads = 32 * (kConsumers + 2);
 constexpr int kItemCost = 2;                 // see attn_sched.cuh
 constexpr int kItems = 8;                    // items that the walking warp may be ahead (more than the tiles it looks up at a time)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMinExp = -200, kMaxExp = 125;   // of V scales: none seen yet, and the largest
-constexpr float kSlack = 8.f;                // the running maximum may lag by this many powers of two
 
 template <int D> __host__ __device__ constexpr int tile_bytes() { return KT * D; }
 template <int D> __host__ __device__ constexpr int stages() { return D == 128 ? 3 : 6; }
@@ -65,18 +56,6 @@ template <int D, int NT, bool PAIR> __host__ __device__ constexpr int smem_bytes
     return 1024 + stages<D>() * 2 * tile_bytes<D>() + shared_bytes<D, NT, PAIR>();
 }
 
-struct TileMeta {
-    float ks[kGroups], vs[kGroups];      // scales of the tile's groups of 16 tokens
-    int have[kGroups];                   // whether the group has a page
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// 2^e, 0 below the smallest normal number, 2^127 above it.
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(min(max(e, -127), 127) + 127) << 23); }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -97,52 +76,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-// Two biased codes (code + 128) of w, chosen by the permutation SEL, as exact fp16.
-template <uint32_t SEL> __device__ __forceinline__ uint32_t codes2(uint32_t w) {
-    const uint32_t v = __byte_perm(w, 0x64646464u, SEL), bias = 0x64806480u;      // 1152
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&bias));
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-            "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-// 4 bytes (or zeros when !have) to shared memory, asynchronously.
-__device__ __forceinline__ void copy4(void *dst, const void *src, bool have) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(have ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// Four consecutive elements as f32.
-__device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-template <class T> __device__ __forceinline__ void load4(const T *p, float (&x)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    const T *e = reinterpret_cast<const T *>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = to_f32(e[i]);
-}
-
-__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-template <class T> __device__ __forceinline__ void store4(T *p, float4 v) {
-    T e[4];
-    from_f32(e[0], v.x);
-    from_f32(e[1], v.y);
-    from_f32(e[2], v.z);
-    from_f32(e[3], v.w);
-    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(e);
-}
-
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_mma(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs p) {
@@ -160,11 +93,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ float red_m[kConsumers][RT], red_l[kConsumers][RT], q_fac[RT];
     __shared__ int q_pos[RT];
     __shared__ int last_part;
+    __shared__ volatile int stop;
 
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *shared = ring + NS * 2 * tile_bytes<D>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        stop = 0;
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1 + kGroups);
             mbar_init(&empty[i], kConsumers);
@@ -333,11 +268,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     int slot = 0;
     uint32_t phase = 0;
     for (uint32_t k = 0;; ++k) {
-        if (!dead && !mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) dead = true;
+        if (!mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) stop = 1;
+        named_sync(1, 32 * kConsumers);              // every warp leaves here, or none
         const Item &it = items[k % kItems];
-        if (dead || it.n == 0) return;
+        if (stop || it.n == 0) return;
         const int y0 = it.y0, n = it.n, pos0 = it.pos0, pos1 = it.pos1, sinks = it.sinks, w0 = it.w0;
-        if (!mbar_wait(&q_full, k & 1u)) dead = true;
+        if (!dead && !mbar_wait(&q_full, k & 1u)) dead = true;
         {
             if constexpr (NT == 1) {
 #pragma unroll
@@ -709,38 +645,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
     }
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
-    static EncodeTiled fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(ptr);
-    });
-    return fn;
-}
-
-// The codes as a tensor of (element, kv head and token of the page, page).
-bool make_map(CUtensorMap *map, const int8_t *codes, const KvView &c) {
-    EncodeTiled enc = encode_fn();
-    if (!enc) return false;
-    const cuuint64_t rows = (cuuint64_t)c.n_kv * c.page;
-    const cuuint64_t dims[3] = {(cuuint64_t)c.d, rows, (cuuint64_t)c.n_pages};
-    const cuuint64_t strides[2] = {(cuuint64_t)c.d, rows * c.d};
-    const cuuint32_t box[3] = {(cuuint32_t)c.d, (cuuint32_t)c.page, 1};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t *>(codes), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class T, int D, int NT> cudaError_t launch(const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {

@@ -164,7 +164,9 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
 
 size_t pq_attn_ws_bytes(int n_q, int n_kv, int d) {
     if (n_q <= 0 || n_kv <= 0 || n_q % n_kv || !head_size_ok(d)) return 0;
-    return d == 64 || d == 128 ? attn_mma_ws_bytes(d) : 16;
+    if (d != 64 && d != 128) return 16;
+    const size_t a = attn_mma_ws_bytes(d), b = attn_tc_ws_bytes(d);
+    return a > b ? a : b;
 }
 
 int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt, const void *q, long long ldq,
@@ -204,8 +206,10 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     a.ws = static_cast<uint8_t *>(ws);
     const int group = a.group.d;
     const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
-    const cudaError_t e = c.d == 64 || c.d == 128 ? launch_attn_mma((int)dt, a, rows, stream, *dev)
-                                                  : launch_attn_generic((int)dt, a, stream);
+    cudaError_t e;
+    if (c.d != 64 && c.d != 128) e = launch_attn_generic((int)dt, a, stream);
+    else if (dt != PQ_F32 && rows > 64) e = launch_attn_tc((int)dt, a, stream, *dev);
+    else e = launch_attn_mma((int)dt, a, rows, stream, *dev);
     return e == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
 }
 

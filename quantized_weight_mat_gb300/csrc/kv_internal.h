@@ -61,6 +61,10 @@ cudaError_t launch_kv_gather(int dt, const KvView &c, void *k_out, long long ldk
 cudaError_t launch_attn_mma(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev);
 size_t attn_mma_ws_bytes(int d);
 unsigned attn_mma_wait_timeouts(bool reset);
+// The same for prompts: 16-bit rows, tensor-core products of 128 rows.
+cudaError_t launch_attn_tc(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev);
+size_t attn_tc_ws_bytes(int d);
+unsigned attn_tc_wait_timeouts(bool reset);
 // Any head size, CUDA cores.
 cudaError_t launch_attn_generic(int dt, const AttnArgs &a, cudaStream_t s);
 
