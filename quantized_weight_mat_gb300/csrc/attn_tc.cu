@@ -8,7 +8,7 @@
 // q' is q scaled per row by a power of two (exact for bf16 and f16), codes are
 // exact in fp16.  A CTA takes 256 rows of one sequence and kv head, as two
 // halves whose products and softmaxes alternate, so that both share one
-// conversion of each K and V tile from 8 bits.
+// conversion of each K and V tile from 8 bits.  P lies over the S it came from.
 //
 // Bound by the tensor cores (4 x 512 cycles a tile for 256 rows at head size
 // 128) and, close to it, by shared memory (operands of four products, 64 KB of
@@ -21,13 +21,20 @@
 //                same image serves as K-major K and as MN-major V)
 //   warp 12      walks the units, TMA of K and V tiles, page numbers and scales
 //   warp 13      one thread issues the products
+//   warp 14      what the softmax needs of a tile's page scales
 // Shared memory: q 64 KB, converted K and V 32 KB each, three raw tiles 96 KB.
 //
 // Per page the weights are formed as exp2(S * f + c), f = q's and K's scales,
 // c = log2(V's scale over a power of two above the largest seen) - maximum:
 // the V scale costs nothing per element; the weight sum undoes it once a page.
 // The running maximum and the power of two lag as in the decode kernel, so O
-// is rescaled (by its own row's thread) only now and then.
+// is rescaled (by its own row's thread) only now and then.  A row goes through
+// tensor memory once, 64 columns at a time; columns that pass the maximum by
+// more than its lag are found beside their weights: the thread then moves the
+// maximum (O, the sum and the row's earlier weights of the tile are rescaled)
+// and takes those columns again.  Tiles at an edge of
+// some row's view, and pages whose scales are no ordinary positive numbers,
+// take a variant that masks and scales element by element.
 
 #include "attn_common.cuh"
 #include "pq_tcgen05.cuh"
@@ -37,8 +44,8 @@ namespace {
 
 constexpr int RT = 256, HALF = 128;          // rows of an item, and of each half
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
-constexpr int kWalkWarp = kSoftmaxWarps + kConvertWarps, kMmaWarp = kWalkWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kWalkWarp = kSoftmaxWarps + kConvertWarps, kMmaWarp = kWalkWarp + 1, kScaleWarp = kWalkWarp + 2;
+constexpr int kThreads = 32 * (kScaleWarp + 1);
 constexpr int kRaw = 3, kMeta = 4, kItems = 8, kItemCost = 2;
 constexpr int kTcGrid = 160;                 // CTAs at most: one per SM
 constexpr int kTmemCols = 512;
@@ -63,21 +70,55 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
+// (x, y) * f + a, and sums of pairs.
+__device__ __forceinline__ void fma2(uint32_t &x, uint32_t &y, float f, float a) {
+    asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n mov.b64 r, {%3, %3};\n"
+        " fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}"
+        : "+r"(x), "+r"(y)
+        : "f"(f), "f"(a));
+}
+__device__ __forceinline__ void add2(float &sx, float &sy, float x, float y) {
+    asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
+        : "+f"(sx), "+f"(sy)
+        : "f"(x), "f"(y));
+}
+
+__device__ __forceinline__ float max3(uint32_t x, uint32_t y, uint32_t z) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(x)), "f"(__uint_as_float(y)), "f"(__uint_as_float(z)));
+    return m;
+}
+
+// A tile's page scales as the softmax takes them.
+struct TileScales {
+    float ks[kGroups], vs[kGroups], lv[kGroups];      // lv = log2(vs)
+    float lv_min;
+    int ve[kGroups];                                  // |vs| < 2^ve; kMinExp for those that take no part
+    int ve_max;
+    int have;                                         // bit g: group g has a page
+    int plain;                                        // every group has one, with ordinary positive scales
+};
+
 // One tile of codes (128 tokens, swizzled as TMA left it) to its fp16 image, by the four converting warps.
 template <int D> __device__ __forceinline__ void convert_tile(uint32_t raw, uint32_t image, int warp, int lane) {
     constexpr int CHUNKS = D / 16, PER = CHUNKS / 4;            // 16-code chunks of a row; a warp takes 8 rows x 4 chunks
 #pragma unroll
-    for (int i = 0; i < 16 * PER / kConvertWarps; ++i) {
-        const int unit = i * kConvertWarps + warp, row = unit / PER * 8 + (lane & 7), c = unit % PER * 4 + (lane >> 3);
-        const int sw = D == 128 ? row & 7 : (row >> 1) & 3;
-        uint4 w = lds128(raw + row * D + ((c ^ sw) << 4));
-        w.x ^= 0x80808080u;
-        w.y ^= 0x80808080u;
-        w.z ^= 0x80808080u;
-        w.w ^= 0x80808080u;
-        const uint32_t to = image + image_at<D>(row, 2 * c);
-        sts128(to, make_uint4(codes2<0x4140>(w.x), codes2<0x4342>(w.x), codes2<0x4140>(w.y), codes2<0x4342>(w.y)));
-        sts128(to + 128, make_uint4(codes2<0x4140>(w.z), codes2<0x4342>(w.z), codes2<0x4140>(w.w), codes2<0x4342>(w.w)));
+    for (int i0 = 0; i0 < 16 * PER / kConvertWarps; i0 += 4) {
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int unit = (i0 + i) * kConvertWarps + warp, row = unit / PER * 8 + (lane & 7), c = unit % PER * 4 + (lane >> 3);
+            const int sw = D == 128 ? row & 7 : (row >> 1) & 3;
+            w[i] = lds128(raw + row * D + ((c ^ sw) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int unit = (i0 + i) * kConvertWarps + warp, row = unit / PER * 8 + (lane & 7), c = unit % PER * 4 + (lane >> 3);
+            const uint32_t x = w[i].x ^ 0x80808080u, y = w[i].y ^ 0x80808080u, z = w[i].z ^ 0x80808080u, v = w[i].w ^ 0x80808080u;
+            const uint32_t to = image + image_at<D>(row, 2 * c);
+            sts128(to, make_uint4(codes2<0x4140>(x), codes2<0x4342>(x), codes2<0x4140>(y), codes2<0x4342>(y)));
+            sts128(to + 128, make_uint4(codes2<0x4140>(z), codes2<0x4342>(z), codes2<0x4140>(v), codes2<0x4342>(v)));
+        }
     }
 }
 
@@ -86,9 +127,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs p) {
     constexpr uint32_t ID_S = instr_desc(HALF, KT), ID_O = instr_desc(HALF, D) | (1u << 16);      // bit 16: B is MN-major
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], meta_full[kMeta], meta_empty[kMeta], i_full[kItems],
+    __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], meta_full[kMeta], meta_empty[kMeta], scales_full[kMeta], i_full[kItems],
         i_empty[kItems], k_ready, k_free, v_ready, v_free, s_full[2], p_ready[2], pv_done[2], q_ready;
     __shared__ __align__(16) TileMeta meta[kMeta];
+    __shared__ __align__(16) TileScales scales[kMeta];
     __shared__ Item items[kItems];
     __shared__ uint32_t tmem_base;
     __shared__ int last_part;
@@ -106,10 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kMeta; ++i) {
             mbar_init(&meta_full[i], 1 + kGroups);
             mbar_init(&meta_empty[i], kSoftmaxWarps);
+            mbar_init(&scales_full[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&i_full[i], 1);
-            mbar_init(&i_empty[i], 3);
+            mbar_init(&i_empty[i], 4);
         }
         mbar_init(&k_ready, kConvertWarps);
         mbar_init(&k_free, 1);
@@ -135,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
-    if (warp == kWalkWarp) {
+    if (warp >= kWalkWarp) {
+        if (warp == kWalkWarp) {
         // ---------------- walk and loads ----------------
         constexpr int BATCH = 32 / kGroups;
         const int g = lane % kGroups, sub = lane / kGroups;
@@ -205,12 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             items[k % kItems].n = 0;
             mbar_arrive(&i_full[k % kItems]);
         }
-    } else if (warp == kMmaWarp) {
+        } else if (warp == kMmaWarp && lane == 0) {
         // ---------------- products ----------------
-        if (lane == 0) {
             uint32_t units = 0, parity[2] = {0u, 0u};
             const uint64_t kd = smem_desc(k0, 128u, 16u * D), vd = smem_desc(v0, 16u * D, 128u);
             uint64_t qd[2];
+#pragma unroll
             for (int h = 0; h < 2; ++h) qd[h] = smem_desc(q0 + h * HALF * D * 2, 128u, 16u * D);
             auto scores = [&](int h) {
 #pragma unroll
@@ -231,10 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&i_empty[k % kItems]);
                 if (!mbar_wait(&q_ready, k & 1u) || !mbar_wait(&k_ready, units & 1u)) break;
                 tc_fence_after();
-                for (int h = 0; h < halves; ++h) scores(h);
+                scores(0);
+                if (halves == 2) scores(1);
                 mma_commit(&k_free);
                 for (int i = 0; i < n && !dead; ++i, ++units) {
-                    for (int h = 0; h < halves; ++h) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (dead || h == halves) break;
                         // P V of this tile, then S of the next one over the same columns
                         if ((h == 0 && !mbar_wait(&v_ready, units & 1u)) || !mbar_wait(&p_ready[h], parity[h])) {
                             dead = true;
@@ -256,6 +303,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (h == halves - 1) mma_commit(&k_free);
                         }
                     }
+                }
+            }
+        } else if (warp == kScaleWarp) {
+        // ---------------- a tile's scales, as the softmax takes them ----------------
+            const int g = lane % kGroups;
+            uint32_t unit = 0;
+            bool dead = false;
+            for (uint32_t k = 0; !dead; ++k) {
+                if (!mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) break;
+                const int n = items[k % kItems].n;
+                __syncwarp();
+                if (n == 0) break;
+                if (lane == 0) mbar_arrive(&i_empty[k % kItems]);
+                for (int i = 0; i < n && !dead; ++i, ++unit) {
+                    const int ms = unit % kMeta;
+                    if (!mbar_wait(&meta_full[ms], (unit / kMeta) & 1u)) dead = true;
+                    const float ks = meta[ms].ks[g], vs = meta[ms].vs[g];
+                    const bool have = meta[ms].have[g] != 0;
+                    const int be = (int)(__float_as_uint(vs) >> 23), bu = be & 255;      // be: with the sign
+                    const bool usable = bu != 0 && bu <= 127 + kMaxExp - 4;
+                    const bool plain = have && usable && be < 256 && ks >= 0.f && ks < INFINITY;
+                    const float lv = lg2(vs);
+                    float lv_min = lv;
+                    const int ve = usable ? bu - 126 : kMinExp;
+                    int ve_max = ve;
+#pragma unroll
+                    for (int w = 1; w < kGroups; w <<= 1) {
+                        lv_min = fminf(lv_min, __shfl_xor_sync(0xffffffffu, lv_min, w));
+                        ve_max = max(ve_max, __shfl_xor_sync(0xffffffffu, ve_max, w));
+                    }
+                    const unsigned haves = __ballot_sync(0xffffffffu, have), plains = __ballot_sync(0xffffffffu, plain);
+                    TileScales &ts = scales[ms];
+                    if (lane < kGroups) {
+                        ts.ks[g] = ks;
+                        ts.vs[g] = vs;
+                        ts.lv[g] = lv;
+                        ts.ve[g] = ve;
+                    }
+                    if (lane == 0) {
+                        ts.lv_min = lv_min;
+                        ts.ve_max = ve_max;
+                        ts.have = (int)(haves & 0xffu);
+                        ts.plain = plains == 0xffffffffu;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&scales_full[ms]);
                 }
             }
         }
@@ -300,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t k = 0;; ++k) {
             if (!mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) stop = 1;
             named_sync(1, 32 * kSoftmaxWarps);            // every warp leaves here, or none
-            const Item it = items[k % kItems];
+            const Item &it = items[k % kItems];           // this group's until it says so below
             if (stop || it.n == 0) break;
             const bool act = it.rows > HALF * half;
             const int r = HALF * half + 32 * (warp & 3) + lane;
@@ -311,25 +404,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (act) {
                 // the row of q: power-of-two scale, fp16, operand image
                 const T *src = static_cast<const T *>(p.q) + (it.r0 + tok) * p.ldq + (long long)head * D;
-                uint4 raw[D / 8];
                 uint32_t top = 0;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) raw[c] = have ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
                     float x[8];
-                    load8(reinterpret_cast<const T *>(&raw[c]), x);
+                    if (have) load8(src + 8 * c, x);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+                    for (int e = 0; e < 8; ++e) top = max(top, have ? __float_as_uint(x[e]) & 0x7fffffffu : 0u);
                 }
                 const int ex = tc_scale_exponent(top);
                 const float up = pow2(ex);
                 fac = pow2(-ex) * (p.scale * kLog2e);
                 const uint32_t dst = q0 + half * HALF * D * 2;
-#pragma unroll
+                // (read again: the row would not fit beside what the loop below keeps)
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
-                    float x[8];
-                    load8(reinterpret_cast<const T *>(&raw[c]), x);
+                    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (have) load8(src + 8 * c, x);
                     sts128(dst + image_at<D>(r - HALF * half, c),
                            make_uint4(pack2(x[0] * up, x[1] * up), pack2(x[2] * up, x[3] * up), pack2(x[4] * up, x[5] * up),
                                       pack2(x[6] * up, x[7] * up)));
@@ -342,126 +433,159 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;
             int vexp = kMinExp;
             for (int y = it.y0; y < it.y0 + it.n; ++y, ++unit) {
-                const TileMeta &mt = meta[unit % kMeta];
-                if (!dead && !mbar_wait(&meta_full[unit % kMeta], (unit / kMeta) & 1u)) dead = true;
+                const TileScales &sc = scales[unit % kMeta];
+                if (!dead && !mbar_wait(&scales_full[unit % kMeta], (unit / kMeta) & 1u)) dead = true;
                 if (act) {
-                    if (!dead && !mbar_wait(&s_full[half], tiles & 1u)) dead = true;
-                    tc_fence_after();
                     const int t0 = (y < it.sinks ? y : it.w0 + (y - it.sinks)) * KT;
-                    bool pages = true;
+                    // the row sees the tile's tokens e with e <= to_pos and (e > to_window or e < to_sink)
+                    const int to_pos = pos - t0, to_window = p.window > 0 ? pos - p.window - t0 : -1, to_sink = p.n_sink - t0;
+                    const bool whole_view = !have || (to_pos >= KT - 1 && (to_window < 0 || to_sink >= KT));
+                    // (V scales at most 2^60 below the reference, which may move to ve_max + 2)
+                    const bool fast = __all_sync(0xffffffffu, whole_view && (!have || sc.lv_min - (float)max(vexp, sc.ve_max + 2) > -60.f)) &&
+                                      sc.plain && p.scale >= 0.f;
+                    // O of the tiles before this one, times the row's a
+                    auto rescale = [&](float a) {
+                        if (y == it.y0) return;
+                        if (!dead && !mbar_wait(&pv_done[half], (tiles + 1) & 1u)) dead = true;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(to + 16 * c, o);
+                            tmem_ld_wait(o);
 #pragma unroll
-                    for (int i = 0; i < kGroups; ++i) pages &= mt.have[i] != 0;
-                    // every row of the warp sees every token (rows that are not there may)
-                    const bool all = __all_sync(0xffffffffu, pages && (!have || (t0 + KT - 1 <= pos && (p.window == 0 || t0 > pos - p.window ||
-                                                                                                       t0 + KT - 1 < p.n_sink))));
-                    auto hides = [&](int t, int g) {
-                        return t > pos || (p.window > 0 && pos - t >= p.window && t >= p.n_sink) || !mt.have[g];
-                    };
-                    // ---- the row's largest score, and the V scales that it sees
-                    float top = -INFINITY;
-                    int big = kMinExp;
-#pragma unroll
-                    for (int c = 0; c < KT / 32; ++c) {
-                        uint32_t s[32];
-                        tmem_ld32(ts + 32 * c, s);
-                        tmem_ld_wait(s);
-#pragma unroll
-                        for (int gi = 0; gi < 2; ++gi) {
-                            const int g = 2 * c + gi;
-                            const float f = mt.ks[g] * fac;
-                            bool sees = have;
-                            if (!all) {
-                                sees = false;
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const bool h = hides(t0 + 16 * g + e, g);
-                                    sees |= !h;
-                                    if (!h) top = fmaxf(top, __uint_as_float(s[16 * gi + e]) * f);
-                                }
-                            } else if (f >= 0.f) {
-                                float x = __uint_as_float(s[16 * gi]);
-#pragma unroll
-                                for (int e = 1; e < 16; ++e) x = fmaxf(x, __uint_as_float(s[16 * gi + e]));
-                                top = fmaxf(top, x * f);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) top = fmaxf(top, __uint_as_float(s[16 * gi + e]) * f);
-                            }
-                            const int be = (int)(__float_as_uint(mt.vs[g]) >> 23) & 255;
-                            if (sees && be != 0 && be <= 127 + kMaxExp - 4) big = max(big, be - 126);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            tmem_st16(to + 16 * c, o);
                         }
+                        tmem_st_wait();
+                    };
+                    // ---- the V scales' reference
+                    int big = kMinExp;
+                    if (fast) {
+                        if (have) big = sc.ve_max;
+                    } else {
+#pragma unroll 1
+                        for (int g = 0; g < kGroups; ++g)
+                            if (((sc.have >> g) & 1) && 16 * g <= to_pos && (min(16 * g + 15, to_pos) > to_window || 16 * g < to_sink))
+                                big = max(big, sc.ve[g]);
                     }
-                    // ---- move the references, rarely
-                    const bool raise = top > m + kSlack || big > vexp;
-                    if (__any_sync(0xffffffffu, raise)) {
+                    if (__any_sync(0xffffffffu, big > vexp)) {
                         float a = 1.f;
-                        const float mn = fmaxf(m, top);
-                        a = m == -INFINITY ? 0.f : ex2(m - mn);
-                        m = mn;
-                        l *= a;
                         if (big > vexp) {
                             big += 2;                 // room to grow
-                            a = vexp == kMinExp ? 0.f : a * pow2(vexp - big);
+                            a = vexp == kMinExp ? 0.f : pow2(vexp - big);
                             vexp = big;
                         }
-                        if (y > it.y0) {
-                            if (!dead && !mbar_wait(&pv_done[half], (tiles + 1) & 1u)) dead = true;
-                            tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(to + 32 * c, o);
-                                tmem_ld_wait(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                                tmem_st32(to + 32 * c, o);
-                            }
-                            tmem_st_wait();
-                        }
+                        rescale(a);
                     }
-                    // ---- weights
-                    const float base = m == -INFINITY ? 0.f : m;
+                    if (!dead && !mbar_wait(&s_full[half], tiles & 1u)) dead = true;
+                    tc_fence_after();
+                    // the row's maximum moves to `top` if that is larger, with c times 16 columns of P in place
+                    auto raise = [&](int c, float top) {
+                        float a = 1.f;
+                        if (top > m) {
+                            a = m == -INFINITY ? 0.f : ex2(m - top);
+                            m = top;
+                        }
+                        l *= a;
+                        rescale(a);
+                        const uint32_t a2 = pack2(a, a);
+#pragma unroll 1
+                        for (int i = 0; i < c; ++i) {
+                            uint32_t w[16];
+                            tmem_st_wait();
+                            tmem_ld16(ts + 16 * i, w);
+                            tmem_ld_wait(w);
 #pragma unroll
-                    for (int c2 = 0; c2 < KT / 64; ++c2) {
-                        uint32_t out[32];
+                            for (int e = 0; e < 16; ++e) {
+                                const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&w[e]), *reinterpret_cast<const __half2 *>(&a2));
+                                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                            tmem_st16(ts + 16 * i, w);
+                        }
+                    };
+                    if (fast) {
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t out[32];
+                            float add;
+                            for (;;) {
+                                uint32_t s[2][32];
+                                tmem_ld32(ts + 64 * c, s[0]);
+                                tmem_ld32(ts + 64 * c + 32, s[1]);
+                                tmem_ld_wait(s[0]);
+                                tmem_ld_wait(s[1]);
+                                const float base = m == -INFINITY ? 0.f : m;
+                                float top = -INFINITY;
+                                add = 0.f;
 #pragma unroll
-                        for (int cc = 0; cc < 2; ++cc) {
-                            uint32_t s[32];
-                            tmem_ld32(ts + 64 * c2 + 32 * cc, s);
-                            tmem_ld_wait(s);
+                                for (int gi = 0; gi < 4; ++gi) {
+                                    const float f = sc.ks[4 * c + gi] * fac, lr = sc.lv[4 * c + gi] - (float)vexp;
+                                    uint32_t *x = &s[gi >> 1][16 * (gi & 1)];
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) fma2(x[e], x[e + 1], f, lr - base);
+                                    float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]);
+#pragma unroll
+                                    for (int e = 6; e < 14; e += 4) {
+                                        a = max3(__float_as_uint(a), x[e], x[e + 1]);
+                                        b = max3(__float_as_uint(b), x[e + 2], x[e + 3]);
+                                    }
+                                    a = max3(__float_as_uint(a), x[14], x[15]);
+                                    top = fmaxf(top, fmaxf(a, b) - lr);
+                                    float sx = 0.f, sy = 0.f;
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) {
+                                        const float wx = ex2(__uint_as_float(x[e])), wy = ex2(__uint_as_float(x[e + 1]));
+                                        add2(sx, sy, wx, wy);
+                                        out[8 * gi + e / 2] = pack2(wx, wy);
+                                    }
+                                    add = fmaf(sx + sy, ex2(-lr), add);
+                                }
+                                // the maximum is passed by more than its lag, or there is none yet: move it, and again
+                                if (!__any_sync(0xffffffffu, top > kSlack || (m == -INFINITY && top > -INFINITY))) break;
+                                raise(2 * c, top + base);
+                            }
+                            l += add;
+                            tmem_st32(ts + 32 * c, out);      // over columns of S that have been read
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t x[32], out[16], seen;
+                            for (;;) {
+                                tmem_ld32(ts + 32 * c, x);
+                                tmem_ld_wait(x);
+                                const float base = m == -INFINITY ? 0.f : m;
+                                float top = -INFINITY;
+                                seen = 0;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const int g = 2 * c + e / 16, te = 32 * c + e;
+                                    const bool see = ((sc.have >> g) & 1) && te <= to_pos && (te > to_window || te < to_sink);
+                                    seen |= see ? 1u << e : 0u;
+                                    x[e] = __float_as_uint(see ? fmaf(__uint_as_float(x[e]), sc.ks[g] * fac, -base) : -INFINITY);
+                                    top = fmaxf(top, __uint_as_float(x[e]));
+                                }
+                                if (!__any_sync(0xffffffffu, top > kSlack || (m == -INFINITY && top > -INFINITY))) break;
+                                raise(c, top + base);
+                            }
 #pragma unroll
                             for (int gi = 0; gi < 2; ++gi) {
-                                const int g = 4 * c2 + 2 * cc + gi;
-                                const float f = mt.ks[g] * fac, vs = mt.vs[g];
-                                const int be = (int)(__float_as_uint(vs) >> 23);      // with the sign: a negative scale is not plain
-                                const float lr = lg2(vs) - (float)vexp;
-                                // the V scale goes into the exponent where it is an ordinary number
-                                const bool plain = __all_sync(0xffffffffu, be != 0 && be <= 127 + kMaxExp - 4 && (lr > -60.f || !have));
-                                float w[16], sum = 0.f;
-                                const float add = plain ? lr - base : -base;
+                                const float vs = sc.vs[2 * c + gi];
+                                const int bu = (int)(__float_as_uint(vs) >> 23) & 255;
+                                const float ratio = bu == 0 ? 0.f : bu > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs * pow2(-vexp);
+                                float w[16];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = ex2(fmaf(__uint_as_float(s[16 * gi + e]), f, add));
-                                if (!all) {
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        if (hides(t0 + 16 * g + e, g)) w[e] = 0.f;
+                                for (int e = 0; e < 16; ++e) {
+                                    const float pr = ex2(__uint_as_float(x[16 * gi + e]));
+                                    l += pr;
+                                    w[e] = (seen >> (16 * gi + e)) & 1 ? pr * ratio : 0.f;      // a hidden page's scale may be NaN
                                 }
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) sum += w[e];
-                                if (plain) {
-                                    l = fmaf(sum, ex2(-lr), l);
-                                } else {
-                                    l += sum;
-                                    const int bu = be & 255;
-                                    const float ratio = bu == 0 ? 0.f : bu > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs * pow2(-vexp);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) w[e] = !all && hides(t0 + 16 * g + e, g) ? 0.f : w[e] * ratio;
-                                }
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) out[16 * cc + 8 * gi + e] = pack2(w[2 * e], w[2 * e + 1]);
+                                for (int e = 0; e < 8; ++e) out[8 * gi + e] = pack2(w[2 * e], w[2 * e + 1]);
                             }
+                            tmem_st16(ts + 16 * c, out);
                         }
-                        tmem_st32(ts + 32 * c2, out);      // over columns of S that have been read
                     }
                     tmem_st_wait();
                     tc_fence_before();
@@ -516,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __threadfence();
                     auto part_of = [&](int c) { return parts + (size_t)(2 * c + (c == it.c0 ? 1 : 0)) * PF; };
                     // a line of threads per row, 4 elements a thread
-                    constexpr int COLS = D / 4, LINES = 32 * kSoftmaxWarps / COLS, AHEAD = 8;
+                    constexpr int COLS = D / 4, LINES = 32 * kSoftmaxWarps / COLS, AHEAD = 2;
                     const int col = threadIdx.x % COLS, line = threadIdx.x / COLS;
                     for (int row = line; row < it.rows; row += LINES) {
                         float pm = -INFINITY, sum = 0.f;
@@ -567,7 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <class T, int D> cudaError_t launch(const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {
     constexpr int smem = smem_bytes<D>();
     static PerDeviceOnce once;
-    cudaError_t e = once.run([] { return cudaFuncSetAttribute(attn_tc<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+    cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(attn_tc<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
     if (!make_map(&km, a.c.k, a.c) || !make_map(&vm, a.c.v, a.c)) return cudaErrorInvalidValue;
