@@ -32,9 +32,8 @@
 // tensor memory once, 64 columns at a time; columns that pass the maximum by
 // more than its lag are found beside their weights: the thread then moves the
 // maximum (O, the sum and the row's earlier weights of the tile are rescaled)
-// and takes those columns again.  Tiles at an edge of
-// some row's view, and pages whose scales are no ordinary positive numbers,
-// take a variant that masks and scales element by element.
+// and takes those columns again.  Tiles at an edge of some row's view, or with
+// page scales that are no ordinary positive numbers, take a masking variant.
 
 #include "attn_common.cuh"
 #include "pq_tcgen05.cuh"
@@ -92,11 +91,11 @@ __device__ __forceinline__ float max3(uint32_t x, uint32_t y, uint32_t z) {
 // A tile's page scales as the softmax takes them.
 struct TileScales {
     float ks[kGroups], vs[kGroups], lv[kGroups];      // lv = log2(vs)
-    float lv_min;
+    float lv_min;                                     // of the plain ones
     int ve[kGroups];                                  // |vs| < 2^ve; kMinExp for those that take no part
     int ve_max;
     int have;                                         // bit g: group g has a page
-    int plain;                                        // every group has one, with ordinary positive scales
+    int plain;                                        // bit g: it does, with ordinary positive scales
 };
 
 // One tile of codes (128 tokens, swizzled as TMA left it) to its fp16 image, by the four converting warps.
@@ -325,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool usable = bu != 0 && bu <= 127 + kMaxExp - 4;
                     const bool plain = have && usable && be < 256 && ks >= 0.f && ks < INFINITY;
                     const float lv = lg2(vs);
-                    float lv_min = lv;
+                    float lv_min = plain ? lv : INFINITY;
                     const int ve = usable ? bu - 126 : kMinExp;
                     int ve_max = ve;
 #pragma unroll
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ts.lv_min = lv_min;
                         ts.ve_max = ve_max;
                         ts.have = (int)(haves & 0xffu);
-                        ts.plain = plains == 0xffffffffu;
+                        ts.plain = (int)(plains & 0xffu);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&scales_full[ms]);
@@ -440,9 +439,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the row sees the tile's tokens e with e <= to_pos and (e > to_window or e < to_sink)
                     const int to_pos = pos - t0, to_window = p.window > 0 ? pos - p.window - t0 : -1, to_sink = p.n_sink - t0;
                     const bool whole_view = !have || (to_pos >= KT - 1 && (to_window < 0 || to_sink >= KT));
-                    // (V scales at most 2^60 below the reference, which may move to ve_max + 2)
-                    const bool fast = __all_sync(0xffffffffu, whole_view && (!have || sc.lv_min - (float)max(vexp, sc.ve_max + 2) > -60.f)) &&
-                                      sc.plain && p.scale >= 0.f;
+                    // V scales in the exponent: at most 2^60 below the reference, which may move to ve_max + 2
+                    const bool near = p.scale >= 0.f && __all_sync(0xffffffffu, !have || sc.lv_min - (float)max(vexp, sc.ve_max + 2) > -60.f);
+                    const bool all = near && __all_sync(0xffffffffu, whole_view) && sc.plain == (1 << kGroups) - 1;
+                    // which of the tokens 32c .. 32c + 31 the row sees
+                    auto view = [&](int c) {
+                        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+                        const uint32_t pages = ((sc.have >> (2 * c)) & 1 ? 0xffffu : 0u) | ((sc.have >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
+                        return pages & below(to_pos + 1 - 32 * c) & (~below(to_window + 1 - 32 * c) | below(to_sink - 32 * c));
+                    };
                     // O of the tiles before this one, times the row's a
                     auto rescale = [&](float a) {
                         if (y == it.y0) return;
@@ -461,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     // ---- the V scales' reference
                     int big = kMinExp;
-                    if (fast) {
+                    if (all) {
                         if (have) big = sc.ve_max;
-                    } else {
+                    } else if (__any_sync(0xffffffffu, sc.ve_max > vexp)) {
 #pragma unroll 1
                         for (int g = 0; g < kGroups; ++g)
                             if (((sc.have >> g) & 1) && 16 * g <= to_pos && (min(16 * g + 15, to_pos) > to_window || 16 * g < to_sink))
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st16(ts + 16 * i, w);
                         }
                     };
-                    if (fast) {
+                    if (all) {
 #pragma unroll 1
                         for (int c = 0; c < 2; ++c) {
                             uint32_t out[32];
@@ -549,41 +554,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st32(ts + 32 * c, out);      // over columns of S that have been read
                         }
                     } else {
+                        // the same at an edge of some row's view, or with other scales
+                        const unsigned plain = near ? (unsigned)sc.plain : 0u;
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32], out[16], seen;
+                            uint32_t out[16];
+                            const uint32_t bits = view(c);
+                            float add;
                             for (;;) {
+                                uint32_t x[32];
                                 tmem_ld32(ts + 32 * c, x);
                                 tmem_ld_wait(x);
                                 const float base = m == -INFINITY ? 0.f : m;
                                 float top = -INFINITY;
-                                seen = 0;
+                                add = 0.f;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const int g = 2 * c + e / 16, te = 32 * c + e;
-                                    const bool see = ((sc.have >> g) & 1) && te <= to_pos && (te > to_window || te < to_sink);
-                                    seen |= see ? 1u << e : 0u;
-                                    x[e] = __float_as_uint(see ? fmaf(__uint_as_float(x[e]), sc.ks[g] * fac, -base) : -INFINITY);
-                                    top = fmaxf(top, __uint_as_float(x[e]));
+                                for (int gi = 0; gi < 2; ++gi) {
+                                    const int g = 2 * c + gi;
+                                    const bool in = (plain >> g) & 1;      // the V scale is in the exponent
+                                    const float f = sc.ks[g] * fac, lr = in ? sc.lv[g] - (float)vexp : 0.f;
+                                    float gm = -INFINITY, w[16], sx = 0.f, sy = 0.f;
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        const bool see = (bits >> (16 * gi + e)) & 1;
+                                        const float y = see ? fmaf(__uint_as_float(x[16 * gi + e]), f, lr - base) : -INFINITY;
+                                        gm = fmaxf(gm, y);
+                                        w[e] = ex2(y);
+                                    }
+                                    top = fmaxf(top, gm - lr);
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) add2(sx, sy, w[e], w[e + 1]);
+                                    add = fmaf(sx + sy, ex2(-lr), add);
+                                    if (!in) {
+                                        const float vs = sc.vs[g];
+                                        const int bu = (int)(__float_as_uint(vs) >> 23) & 255;
+                                        const float ratio = bu == 0 ? 0.f : bu > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs * pow2(-vexp);
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) w[e] = (bits >> (16 * gi + e)) & 1 ? w[e] * ratio : 0.f;      // the ratio may be NaN
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) out[8 * gi + e] = pack2(w[2 * e], w[2 * e + 1]);
                                 }
                                 if (!__any_sync(0xffffffffu, top > kSlack || (m == -INFINITY && top > -INFINITY))) break;
                                 raise(c, top + base);
                             }
-#pragma unroll
-                            for (int gi = 0; gi < 2; ++gi) {
-                                const float vs = sc.vs[2 * c + gi];
-                                const int bu = (int)(__float_as_uint(vs) >> 23) & 255;
-                                const float ratio = bu == 0 ? 0.f : bu > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs * pow2(-vexp);
-                                float w[16];
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const float pr = ex2(__uint_as_float(x[16 * gi + e]));
-                                    l += pr;
-                                    w[e] = (seen >> (16 * gi + e)) & 1 ? pr * ratio : 0.f;      // a hidden page's scale may be NaN
-                                }
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) out[8 * gi + e] = pack2(w[2 * e], w[2 * e + 1]);
-                            }
+                            l += add;
                             tmem_st16(ts + 16 * c, out);
                         }
                     }
