@@ -369,9 +369,9 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
  *   q     device [n_rows][n_q * d] of type dt, row stride ldq (elements)
  *   out   device [n_rows][n_q * d] of type dt, row stride ldo; overlaps
  *         neither q nor the cache
- *   ws    device, 16-byte aligned, at least pq_attn_ws_bytes(...) bytes, zeros
- *         before its first use; every call leaves it ready for the next.
- *         Calls that may overlap on the GPU need one each.
+ *   ws    device, 16-byte aligned, at least pq_attn_ws_bytes(...) bytes; what it
+ *         holds before and after a call does not matter.  Calls that may
+ *         overlap on the GPU need one each.
  * Accumulation in f32; q and the softmax weights enter the tensor cores as fp16
  * (f32 rows: as fp16 pairs), the codes exactly.  Deterministic.
  */

@@ -59,6 +59,8 @@ class PQError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libpq.so (built by ``build.build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -117,10 +119,27 @@ def _addr(p) -> int:
     return int(p.data_ptr())
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream (by its raw-handle query: a tenth of the cost of a Stream object)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if query is None:
+            _raw_stream = lambda: int(torch.cuda.current_stream().cuda_stream)  # noqa: E731
+        else:
+            torch.cuda.init()
+            device = torch.cuda.current_device
+            _raw_stream = lambda: query(device())  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

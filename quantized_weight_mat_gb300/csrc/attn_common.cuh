@@ -106,5 +106,94 @@ bool make_map(CUtensorMap *map, const int8_t *codes, const KvView &c) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Joins the parts of the item that CTA blockIdx.x of an attention kernel began,
+// up to 32 rows a block: a line of threads per row, 4 elements a thread, the
+// parts in CTA order.
+template <class T, int D, int RT> __global__ void __launch_bounds__(256) attn_join(AttnArgs p) {
+    constexpr int COLS = D / 4, LINES = 256 / COLS, BLOCK = RT < 32 ? RT : 32;
+    constexpr int ROWS = BLOCK > LINES ? BLOCK / LINES : 1, AHEAD = ROWS > 2 ? 4 : 8;
+    constexpr size_t PF = attn_part_floats(RT, D);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int c0 = blockIdx.x;
+    const Split it = splits_of(p)[c0];
+    const int col = threadIdx.x % COLS, line = threadIdx.x / COLS, row0 = BLOCK * blockIdx.y + line;
+    if (it.c1 < 0 || line >= BLOCK || row0 >= it.rows) return;
+    const float *parts = parts_of(p);
+    float m[ROWS], sum[ROWS];
+    float4 acc[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        m[r] = -INFINITY;
+        sum[r] = 0.f;
+        acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int c = c0; c <= it.c1; c += AHEAD) {
+        float2 ml[AHEAD][ROWS];
+        float4 v[AHEAD][ROWS];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const int row = row0 + r * LINES;
+                ml[i][r] = make_float2(-INFINITY, 0.f);
+                if (c + i > it.c1 || row >= it.rows) continue;
+                // the first CTA's part is the item its range ends in, the others' the one theirs starts in
+                const float *pp = parts + (size_t)(2 * (c + i) + (c + i == c0 ? 1 : 0)) * PF;
+                ml[i][r] = __ldcg(reinterpret_cast<const float2 *>(pp + (size_t)RT * D) + row);
+                v[i][r] = __ldcg(reinterpret_cast<const float4 *>(pp + (size_t)row * D) + col);
+            }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const float mn = fmaxf(m[r], ml[i][r].x);
+                if (ml[i][r].x == -INFINITY) {
+                    sum[r] += ml[i][r].y;      // nothing, or NaN
+                    continue;
+                }
+                const float a = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn), b = ex2(ml[i][r].x - mn);
+                m[r] = mn;
+                sum[r] = sum[r] * a + ml[i][r].y * b;
+                acc[r].x = acc[r].x * a + v[i][r].x * b;
+                acc[r].y = acc[r].y * a + v[i][r].y * b;
+                acc[r].z = acc[r].z * a + v[i][r].z * b;
+                acc[r].w = acc[r].w * a + v[i][r].w * b;
+            }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int row = row0 + r * LINES;
+        if (row >= it.rows) break;
+        const float inv = sum[r] != 0.f ? 1.f / sum[r] : 0.f;
+        const int tk = p.group.div(it.j * RT + row), hd = it.h * p.group.d + it.j * RT + row - tk * p.group.d;
+        store4(static_cast<T *>(p.out) + (it.r0 + tk) * p.ldo + (long long)hd * D + 4 * col,
+               make_float4(acc[r].x * inv, acc[r].y * inv, acc[r].z * inv, acc[r].w * inv));
+    }
+}
+
+// Launches an attention kernel and the join of its parts, each so that it may be
+// scheduled while the kernel before it finishes.
+template <class T, int D, int RT, class K>
+cudaError_t launch_with_join(K kernel, unsigned grid, int threads, int smem, const CUtensorMap &km, const CUtensorMap &vm,
+                             const AttnArgs &a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, km, vm, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim.y = RT > 32 ? RT / 32 : 1;
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attn_join<T, D, RT>, a);
+}
+
 }  // namespace
 }  // namespace pqk

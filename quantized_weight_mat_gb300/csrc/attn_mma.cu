@@ -92,7 +92,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ long long q_out[RT];
     __shared__ float red_m[kConsumers][RT], red_l[kConsumers][RT], q_fac[RT];
     __shared__ int q_pos[RT];
-    __shared__ int last_part;
     __shared__ volatile int stop;
 
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -183,7 +182,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int g = lane % kGroups, sub = lane / kGroups;
         Walk at;
         long long first, last;
-        const Cut cut = find_range<Walk, kItemCost>(p, at, first, last);
+        const Cut cut = find_range<Walk, kItemCost + 1>(p, at, first, last);
+        Split *split = splits_of(p) + blockIdx.x;
+        if (lane == 0) split->c1 = -1;
         int slot = 0;
         uint32_t phase = 1, k = 0;
         bool fresh = true;
@@ -196,8 +197,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     fresh = false;
                     if (!mbar_wait(&i_empty[k % kItems], (k / kItems + 1) & 1u)) return;
                     if (lane == 0) {
-                        items[k % kItems] = item_of(at, cut, first, last);
+                        const Item it = item_of(at, cut, first, last);
+                        items[k % kItems] = it;
                         mbar_arrive(&i_full[k % kItems]);
+                        if (it.c0 == (int)blockIdx.x && it.c1 > it.c0) *split = Split{it.c1, it.rows, it.r0, it.j, it.h};
                     }
                     ++k;
                 }
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int tid = threadIdx.x, rows = it.rows;
             constexpr int COLS = D / 4;                      // groups of 4 elements
             const int col = tid % COLS, line = tid / COLS;
-            float *parts = reinterpret_cast<float *>(p.ws + attn_counter_bytes());
+            float *parts = parts_of(p);
             constexpr size_t PF = attn_part_floats(RT, D);
             float *part = parts + (size_t)it.slot * PF;
             // 4 elements of a row of the item
@@ -584,60 +587,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     named_sync(1, 32 * kConsumers);
                 }
-            if (!whole) {
-                // ---------------- join the CTAs' parts ----------------
-                const int c0 = it.c0, c1 = it.c1;
-                unsigned *counter = reinterpret_cast<unsigned *>(p.ws) + c0;
-                __threadfence();
-                named_sync(1, 32 * kConsumers);
-                if (tid == 0) {
-                    const bool is_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
-                    if (is_last) *counter = 0u;          // ready for the next call
-                    last_part = is_last;
-                }
-                named_sync(1, 32 * kConsumers);
-                if (last_part) {
-                    __threadfence();
-                    auto part_of = [&](int c) { return parts + (size_t)(2 * c + (c == c0 ? 1 : 0)) * PF; };
-                    // a line of threads per row, 4 elements a thread; the loads of 16 parts are in flight together
-                    constexpr int LINES = 32 * kConsumers / COLS, AHEAD = 16;
-                    for (int row = line; row < rows; row += LINES) {
-                        float top = -INFINITY, sum = 0.f;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int c = c0; c <= c1; c += AHEAD) {
-                            float2 ml[AHEAD];
-                            float4 v[AHEAD];
-#pragma unroll
-                            for (int i = 0; i < AHEAD; ++i) {
-                                const float *pp = part_of(min(c + i, c1));
-                                ml[i] = __ldcg(reinterpret_cast<const float2 *>(pp + RT * D) + row);
-                                v[i] = __ldcg(reinterpret_cast<const float4 *>(pp + row * D) + col);
-                            }
-                            float mn = top;
-#pragma unroll
-                            for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, ml[i].x);
-                            const float a = top == -INFINITY ? 0.f : ex2(top - mn);
-                            top = mn;
-                            sum *= a;
-                            acc.x *= a;
-                            acc.y *= a;
-                            acc.z *= a;
-                            acc.w *= a;
-#pragma unroll
-                            for (int i = 0; i < AHEAD; ++i) {
-                                const float f = c + i > c1 || ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - top);
-                                if (c + i > c1) continue;
-                                sum += ml[i].y * f;
-                                acc.x += v[i].x * f;
-                                acc.y += v[i].y * f;
-                                acc.z += v[i].z * f;
-                                acc.w += v[i].w * f;
-                            }
-                        }
-                        put(row, acc, sum);
-                    }
-                }
-            }
             named_sync(1, 32 * kConsumers);                  // the item and the buffer are free
             if (tid == 0) {
                 mbar_arrive(&q_empty);
@@ -662,17 +611,7 @@ template <class T, int D, int NT> cudaError_t launch(const AttnArgs &a, cudaStre
     long long grid = 2 * dev.sm_count;
     if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
     if (row_tiles < grid && tiles * row_tiles * a.c.n_kv < grid) grid = tiles * row_tiles * a.c.n_kv;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_mma<T, D, NT>, km, vm, a);
+    return launch_with_join<T, D, 8 * NT>(attn_mma<T, D, NT>, (unsigned)grid, kThreads, smem, km, vm, a, s);
 }
 
 template <class T> cudaError_t launch_t(const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
@@ -692,7 +631,7 @@ unsigned attn_mma_wait_timeouts(bool reset) {
     return v;
 }
 
-size_t attn_mma_ws_bytes(int d) { return attn_counter_bytes() + 2 * kAttnMaxGrid * attn_part_floats(16, d) * 4; }
+size_t attn_mma_ws_bytes(int d) { return attn_splits_bytes() + 2 * kAttnMaxGrid * attn_part_floats(16, d) * 4; }
 
 cudaError_t launch_attn_mma(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
     if (dt == PQ_F32) return launch_t<float>(a, rows, s, dev);

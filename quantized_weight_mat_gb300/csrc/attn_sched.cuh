@@ -10,7 +10,8 @@
 // places, in the order sequence, kv head, row tile, token tile, are cut into
 // one contiguous equal range per CTA, so that long and short sequences load every CTA
 // alike; an item cut by a range's end is joined from its CTAs' parts, in CTA
-// order, by whichever of them is the last to finish.
+// order, by a second small kernel (one SM reading all parts of an item of a long
+// sequence took 6 us of 52, and the last CTA's fence and counter 1 us of every split).
 #pragma once
 
 #include "kv_device.cuh"
@@ -53,9 +54,9 @@ struct Cut {
     long long total, size, longer;
     int grid;                         // ranges: CTAs that have work
 
-    // At most `most` ranges, each with at least one unit.
-    __device__ __forceinline__ Cut(long long total_, int most, int cost) : total(total_) {
-        grid = (int)min((long long)most, max(div_places(total, cost + 1), 1ll));
+    // At most `most` ranges, of at least `least` places (more than an item's cost, so that each has a unit).
+    __device__ __forceinline__ Cut(long long total_, int most, int least) : total(total_) {
+        grid = (int)min((long long)most, max(div_places(total, least), 1ll));
         size = div_places(total, grid);
         longer = total - size * grid;
     }
@@ -125,9 +126,10 @@ template <class Walk> __device__ __forceinline__ long long warp_places(const Att
     return walk.m > 0 ? walk.places(p) : 0;
 }
 
-// By one warp: the places of the call, and `walk` at the first unit of CTA
-// blockIdx.x's range [first, last); first == last when it has none.
-template <class Walk, int COST>
+// By one warp: the places of the call, cut into ranges of at least LEAST, and
+// `walk` at the first unit of CTA blockIdx.x's range [first, last); first ==
+// last when it has none.
+template <class Walk, int LEAST>
 __device__ __forceinline__ Cut find_range(const AttnArgs &p, Walk &walk, long long &first, long long &last) {
     const int lane = threadIdx.x & 31, n_seq = p.c.n_seq;
     long long total = 0, incl = 0, mine = 0;
@@ -142,7 +144,7 @@ __device__ __forceinline__ Cut find_range(const AttnArgs &p, Walk &walk, long lo
         incl += total;
         total = __shfl_sync(0xffffffffu, incl, 31);
     }
-    const Cut cut(total * p.c.n_kv, (int)gridDim.x, COST);
+    const Cut cut(total * p.c.n_kv, (int)gridDim.x, LEAST);
     first = last = 0;
     if (total == 0 || (int)blockIdx.x >= cut.grid) return cut;
     first = cut.begin(blockIdx.x);
@@ -210,11 +212,16 @@ __device__ __forceinline__ Item item_of(const Walk &at, const Cut &cut, long lon
     return it;
 }
 
-// Workspace: counters of the items that several CTAs share (item counter =
-// index of its first CTA; zero between calls), then two parts per CTA (slot 2c:
-// an item that began in an earlier CTA, 2c + 1: one that begins here and goes
-// on).  A part is RT x D f32 sums, then RT pairs of a maximum and a weight sum.
-__host__ __device__ constexpr size_t attn_counter_bytes() { return (size_t)kAttnMaxGrid * 4; }
+// Workspace: one Split per CTA, then two parts per CTA (slot 2c: an item that
+// began in an earlier CTA, 2c + 1: one that begins here and goes on).  A part is
+// RT x D f32 sums, then RT pairs of a maximum and a weight sum.  Nothing in it
+// outlives the call.
+struct Split {
+    int c1, rows, r0, j, h;      // the item that begins here and goes on, to CTA c1 (-1: none does)
+};
+__host__ __device__ constexpr size_t attn_splits_bytes() { return (kAttnMaxGrid * sizeof(Split) + 15) / 16 * 16; }
 __host__ __device__ constexpr size_t attn_part_floats(int rt, int d) { return (size_t)rt * (d + 2); }   // a multiple of 4 (rt is one of 8)
+__device__ __forceinline__ Split *splits_of(const AttnArgs &p) { return reinterpret_cast<Split *>(p.ws); }
+__device__ __forceinline__ float *parts_of(const AttnArgs &p) { return reinterpret_cast<float *>(p.ws + attn_splits_bytes()); }
 
 }  // namespace pqk

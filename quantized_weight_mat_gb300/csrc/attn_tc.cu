@@ -46,6 +46,7 @@ constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kWalkWarp = kSoftmaxWarps + kConvertWarps, kMmaWarp = kWalkWarp + 1, kScaleWarp = kWalkWarp + 2;
 constexpr int kThreads = 32 * (kScaleWarp + 1);
 constexpr int kRaw = 3, kMeta = 4, kItems = 8, kItemCost = 2;
+constexpr int kLeast = 4;                    // places of a CTA
 constexpr int kTcGrid = 160;                 // CTAs at most: one per SM
 constexpr int kTmemCols = 512;
 using Walk = UnitWalk<RT, KT, kItemCost>;
@@ -132,7 +133,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(16) TileScales scales[kMeta];
     __shared__ Item items[kItems];
     __shared__ uint32_t tmem_base;
-    __shared__ int last_part;
     __shared__ volatile int stop, stop_convert;
 
     // converted V and K, q, raw tiles, from a 1024-byte boundary
@@ -184,7 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = lane % kGroups, sub = lane / kGroups;
         Walk at;
         long long first, last;
-        const Cut cut = find_range<Walk, kItemCost>(p, at, first, last);
+        const Cut cut = find_range<Walk, kLeast>(p, at, first, last);
+        Split *split = splits_of(p) + blockIdx.x;
+        if (lane == 0) split->c1 = -1;
         uint32_t k = 0, n_unit = 0;
         bool fresh = true, dead = false;
         at.w = first == last ? last : at.w;
@@ -196,8 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fresh = false;
                     if (!mbar_wait(&i_empty[k % kItems], (k / kItems + 1) & 1u)) dead = true;
                     if (lane == 0 && !dead) {
-                        items[k % kItems] = item_of(at, cut, first, last);
+                        const Item it = item_of(at, cut, first, last);
+                        items[k % kItems] = it;
                         mbar_arrive(&i_full[k % kItems]);
+                        if (it.c0 == (int)blockIdx.x && it.c1 > it.c0) *split = Split{it.c1, it.rows, it.r0, it.j, it.h};
                     }
                     ++k;
                 }
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---------------- the item's end ----------------
             const bool whole = it.c0 == it.c1;
-            float *parts = reinterpret_cast<float *>(p.ws + attn_counter_bytes());
+            float *parts = parts_of(p);
             constexpr size_t PF = attn_part_floats(RT, D);
             T *out = static_cast<T *>(p.out) + (it.r0 + tok) * p.ldo + (long long)head * D;
             if (act) {
@@ -641,55 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!whole && have) *reinterpret_cast<float2 *>(parts + (size_t)it.slot * PF + (size_t)RT * D + 2 * r) = make_float2(m, l);
                 tc_fence_before();
             }
-            if (!whole) {
-                unsigned *counter = reinterpret_cast<unsigned *>(p.ws) + it.c0;
-                __threadfence();
-                named_sync(1, 32 * kSoftmaxWarps);
-                if (threadIdx.x == 0) {
-                    const bool is_last = atomicAdd(counter, 1u) == (unsigned)(it.c1 - it.c0);
-                    if (is_last) *counter = 0u;          // ready for the next call
-                    last_part = is_last;
-                }
-                named_sync(1, 32 * kSoftmaxWarps);
-                if (last_part) {
-                    __threadfence();
-                    auto part_of = [&](int c) { return parts + (size_t)(2 * c + (c == it.c0 ? 1 : 0)) * PF; };
-                    // a line of threads per row, 4 elements a thread
-                    constexpr int COLS = D / 4, LINES = 32 * kSoftmaxWarps / COLS, AHEAD = 2;
-                    const int col = threadIdx.x % COLS, line = threadIdx.x / COLS;
-                    for (int row = line; row < it.rows; row += LINES) {
-                        float pm = -INFINITY, sum = 0.f;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int c = it.c0; c <= it.c1; c += AHEAD) {
-                            float2 ml[AHEAD];
-                            float4 v[AHEAD];
-#pragma unroll
-                            for (int i = 0; i < AHEAD; ++i) {
-                                if (c + i > it.c1) continue;
-                                const float *pp = part_of(c + i);
-                                ml[i] = __ldcg(reinterpret_cast<const float2 *>(pp + (size_t)RT * D) + row);
-                                v[i] = __ldcg(reinterpret_cast<const float4 *>(pp + (size_t)row * D) + col);
-                            }
-#pragma unroll
-                            for (int i = 0; i < AHEAD; ++i) {
-                                if (c + i > it.c1) continue;
-                                const float mn = fmaxf(pm, ml[i].x);
-                                const float a = pm == -INFINITY ? 0.f : ex2(pm - mn), b = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - mn);
-                                pm = mn;
-                                sum = sum * a + ml[i].y * b;
-                                acc.x = acc.x * a + v[i].x * b;
-                                acc.y = acc.y * a + v[i].y * b;
-                                acc.z = acc.z * a + v[i].z * b;
-                                acc.w = acc.w * a + v[i].w * b;
-                            }
-                        }
-                        const float inv = sum != 0.f ? 1.f / sum : 0.f;
-                        const int tk = p.group.div(it.j * RT + row), hd = it.h * p.group.d + it.j * RT + row - tk * p.group.d;
-                        store4(static_cast<T *>(p.out) + (it.r0 + tk) * p.ldo + (long long)hd * D + 4 * col,
-                               make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-                    }
-                }
-            }
             named_sync(1, 32 * kSoftmaxWarps);
             if (threadIdx.x == 0) mbar_arrive(&i_empty[k % kItems]);
         }
@@ -712,17 +667,7 @@ template <class T, int D> cudaError_t launch(const AttnArgs &a, cudaStream_t s, 
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
     if (!make_map(&km, a.c.k, a.c) || !make_map(&vm, a.c.v, a.c)) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(dev.sm_count < kTcGrid ? dev.sm_count : kTcGrid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tc<T, D>, km, vm, a);
+    return launch_with_join<T, D, RT>(attn_tc<T, D>, (unsigned)(dev.sm_count < kTcGrid ? dev.sm_count : kTcGrid), kThreads, smem, km, vm, a, s);
 }
 
 }  // namespace
@@ -737,7 +682,7 @@ unsigned attn_tc_wait_timeouts(bool reset) {
     return v;
 }
 
-size_t attn_tc_ws_bytes(int d) { return attn_counter_bytes() + 2 * kTcGrid * attn_part_floats(RT, d) * 4; }
+size_t attn_tc_ws_bytes(int d) { return attn_splits_bytes() + 2 * kTcGrid * attn_part_floats(RT, d) * 4; }
 
 cudaError_t launch_attn_tc(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {
     if (dt == PQ_F16) return a.c.d == 128 ? launch<__half, 128>(a, s, dev) : launch<__half, 64>(a, s, dev);

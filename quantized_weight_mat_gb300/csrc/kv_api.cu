@@ -113,6 +113,7 @@ int pq_kv_append(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
         if (n_q <= 0) return PQ_ERR_ARG;
         if (n_q % c.n_kv) return PQ_ERR_LAYOUT;
         const int64_t qw = (int64_t)n_q * c.d;
+        if (n_rows * (qw / 16) > (INT64_C(1) << 30)) return PQ_ERR_SIZE;
         if ((st = check_rows(q, ldq, qw, n_rows, eb)) || (st = check_rows(q_out, ldqo, qw, n_rows, eb))) return st;
         const int64_t ob = rows_bytes(ldqo, qw, n_rows, eb);
         const bool in_place = q_out == q && ldqo == ldq;
@@ -141,6 +142,8 @@ int pq_kv_append(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
     a.n_pos = n_pos;
     a.rot = rot;
     a.pair = rope_mode == PQ_ROPE_PAIR;
+    a.units = FastDiv(c.d / 16);
+    a.per_row = FastDiv(q ? n_q * (c.d / 16) : 1);
     return launch_kv_append((int)dt, a, stream) == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
 }
 
@@ -208,7 +211,7 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
     cudaError_t e;
     if (c.d != 64 && c.d != 128) e = launch_attn_generic((int)dt, a, stream);
-    else if (dt != PQ_F32 && rows > 64) e = launch_attn_tc((int)dt, a, stream, *dev);
+    else if (dt != PQ_F32 && rows > 32) e = launch_attn_tc((int)dt, a, stream, *dev);
     else e = launch_attn_mma((int)dt, a, rows, stream, *dev);
     return e == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
 }

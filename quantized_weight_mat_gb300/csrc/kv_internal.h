@@ -17,15 +17,6 @@ struct KvView {
     int n_rows;
 };
 
-struct KvAppendArgs {
-    KvView c;
-    const void *k, *v, *q;
-    void *q_out;
-    long long ldk, ldv, ldq, ldqo;
-    const float *cos, *sin;
-    int n_q, n_pos, rot, pair;   // pair: rotate (2i, 2i+1) instead of (i, i + rot/2)
-};
-
 // Quotients by a divisor known on the host, exact for 0 <= n < 2^31:
 // n / d = (mulhi(n, magic) + n) >> shift with shift = ceil(log2 d) and magic =
 // floor(2^32 (2^shift - d) / d) + 1 (Granlund and Montgomery, 1994).
@@ -39,6 +30,16 @@ struct FastDiv {
 #ifdef __CUDACC__
     __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((unsigned)n, magic) + (unsigned)n) >> shift); }
 #endif
+};
+
+struct KvAppendArgs {
+    KvView c;
+    const void *k, *v, *q;
+    void *q_out;
+    long long ldk, ldv, ldq, ldqo;
+    const float *cos, *sin;
+    int n_q, n_pos, rot, pair;   // pair: rotate (2i, 2i+1) instead of (i, i + rot/2)
+    FastDiv units, per_row;      // d / 16, and n_q times that
 };
 
 struct AttnArgs {
