@@ -372,8 +372,9 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
  *   ws    device, 16-byte aligned, at least pq_attn_ws_bytes(...) bytes; what it
  *         holds before and after a call does not matter.  Calls that may
  *         overlap on the GPU need one each.
- * Accumulation in f32; q and the softmax weights enter the tensor cores as fp16
- * (f32 rows: as fp16 pairs), the codes exactly.  Deterministic.
+ * Accumulation in f32; q (scaled per row by a power of two) and the softmax
+ * weights enter the tensor cores as fp16, f32 rows' as fp16 pairs, the codes
+ * exactly.  Deterministic.
  */
 int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt,
             const void *q, long long ldq, int n_q, float scale, int window, int n_sink,

@@ -175,10 +175,11 @@ template <class T, int D, int RT> __global__ void __launch_bounds__(256) attn_jo
 // Launches an attention kernel and the join of its parts, each so that it may be
 // scheduled while the kernel before it finishes.
 template <class T, int D, int RT, class K>
-cudaError_t launch_with_join(K kernel, unsigned grid, int threads, int smem, const CUtensorMap &km, const CUtensorMap &vm,
-                             const AttnArgs &a, cudaStream_t s) {
+cudaError_t launch_with_join(K kernel, int grid, int threads, int smem, const CUtensorMap &km, const CUtensorMap &vm,
+                             AttnArgs a, cudaStream_t s) {
+    a.grid = FastDiv(grid);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;

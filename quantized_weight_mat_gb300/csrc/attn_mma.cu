@@ -11,7 +11,9 @@
 // they can be: int8 codes become fp16 by a byte permute and one subtraction
 // (0x6400 | (code + 128) is 1152 + code); q is scaled per row by a power of
 // two into fp16's range (one fp16 for 16-bit rows, an fp16 pair for f32 rows).
-// The softmax weights enter in fp16 (f32 rows: an fp16 pair), already times
+// The softmax weights enter in fp16 for bf16 rows (their 11 bits lie far below
+// the output's 8) and as an fp16 pair for f16 and f32 rows (one fp16 would add half
+// as much again to f16's own rounding, and the loads hide the second product), already times
 // their page's V scale over a power of two above the largest one the row has
 // seen: ratios are at most 1 and weights at most the 2^8 that the running
 // maximum may lag behind, so fp16 holds them whatever the scales.  Both
@@ -30,6 +32,8 @@
 // the present item runs; warps 0-3 take 32 tokens of a tile each, as two independent
 // groups of 16, with a running maximum of their own, and join at the end of
 // an item.
+
+#include <type_traits>
 
 #include "attn_common.cuh"
 
@@ -80,8 +84,9 @@ template <class T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_mma(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs p) {
     constexpr int RT = 8 * NT, NS = stages<D>(), CH = D / 16;
-    constexpr bool PAIR = sizeof(T) == 4;            // q and the weights as fp16 pairs
-    constexpr int kLiftExp = PAIR ? 7 : 0;           // keeps the low halves of small weights above fp16's last bit
+    constexpr bool PAIR = sizeof(T) == 4;            // q as fp16 pairs
+    constexpr bool WPAIR = !std::is_same<T, __nv_bfloat16>::value;      // the weights as fp16 pairs
+    constexpr int kLiftExp = WPAIR ? 7 : 0;          // keeps the low halves of small weights above fp16's last bit
     constexpr int RLD = red_pitch<D>(), QP = q_pitch<D>();
     constexpr int AHEAD_C = NT == 1 ? CH / 2 : 1;    // K chunk pairs loaded ahead of their use
     using Walk = UnitWalk<RT, KT, kItemCost>;
@@ -183,8 +188,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         Walk at;
         long long first, last;
         const Cut cut = find_range<Walk, kItemCost + 1>(p, at, first, last);
-        Split *split = splits_of(p) + blockIdx.x;
-        if (lane == 0) split->c1 = -1;
+        Split split;                       // of the last item: only that can go on in another CTA
+        split.c1 = -1;
+        if (lane == 0) splits_of(p)[blockIdx.x].c1 = -1;      // should a wait below run out
         int slot = 0;
         uint32_t phase = 1, k = 0;
         bool fresh = true;
@@ -197,10 +203,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     fresh = false;
                     if (!mbar_wait(&i_empty[k % kItems], (k / kItems + 1) & 1u)) return;
                     if (lane == 0) {
-                        const Item it = item_of(at, cut, first, last);
-                        items[k % kItems] = it;
+                        items[k % kItems] = item_of(at, first, last);
                         mbar_arrive(&i_full[k % kItems]);
-                        if (it.c0 == (int)blockIdx.x && it.c1 > it.c0) *split = Split{it.c1, it.rows, it.r0, it.j, it.h};
                     }
                     ++k;
                 }
@@ -209,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     seq = at.s;
                     head = at.h;
                 }
+                if (at.w + 1 == last) split = split_of(at, cut, first, last);
                 if (at.y + 1 < at.t.units) {
                     ++at.y;
                     ++at.w;
@@ -243,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
         }
+        if (lane == 0) splits_of(p)[blockIdx.x] = split;
         if (!mbar_wait(&i_empty[k % kItems], (k / kItems + 1) & 1u)) return;
         if (lane == 0) {
             items[k % kItems].n = 0;
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int x = 0; x < NT; ++x)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) vinv[x][e] = pow2(kLiftExp - vexp[x][e]);
-            uint32_t ph[2][NT][2], pl[2][PAIR ? NT : 1][2];
+            uint32_t ph[2][NT][2], pl[2][WPAIR ? NT : 1][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t hi = pack2(w[2 * e], w[2 * e + 1]);
                         ph[i][x][e] = transpose8x8(hi);
-                        if constexpr (PAIR) {
+                        if constexpr (WPAIR) {
                             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
                             pl[i][x][e] = transpose8x8(pack2(w[2 * e] - f.x, w[2 * e + 1] - f.y));
                         }
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int x = 0; x < NT; ++x) {
                             mma(o[x][2 * c2 + e], a, ph[i][x][0], ph[i][x][1]);
-                            if constexpr (PAIR) mma(o[x][2 * c2 + e], a, pl[i][x][0], pl[i][x][1]);
+                            if constexpr (WPAIR) mma(o[x][2 * c2 + e], a, pl[i][x][0], pl[i][x][1]);
                         }
                     }
                 }
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
         // ---------------- the item's end: join the four warps ----------------
         {
-            const bool whole = it.c0 == it.c1;
+            const bool whole = it.whole;
             const int tid = threadIdx.x, rows = it.rows;
             constexpr int COLS = D / 4;                      // groups of 4 elements
             const int col = tid % COLS, line = tid / COLS;
@@ -611,7 +617,7 @@ template <class T, int D, int NT> cudaError_t launch(const AttnArgs &a, cudaStre
     long long grid = 2 * dev.sm_count;
     if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
     if (row_tiles < grid && tiles * row_tiles * a.c.n_kv < grid) grid = tiles * row_tiles * a.c.n_kv;
-    return launch_with_join<T, D, 8 * NT>(attn_mma<T, D, NT>, (unsigned)grid, kThreads, smem, km, vm, a, s);
+    return launch_with_join<T, D, 8 * NT>(attn_mma<T, D, NT>, (int)grid, kThreads, smem, km, vm, a, s);
 }
 
 template <class T> cudaError_t launch_t(const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {

@@ -54,11 +54,19 @@ struct Cut {
     long long total, size, longer;
     int grid;                         // ranges: CTAs that have work
 
-    // At most `most` ranges, of at least `least` places (more than an item's cost, so that each has a unit).
-    __device__ __forceinline__ Cut(long long total_, int most, int least) : total(total_) {
-        grid = (int)min((long long)most, max(div_places(total, least), 1ll));
-        size = div_places(total, grid);
-        longer = total - size * grid;
+    // At most `most` ranges, of at least LEAST places (more than an item's cost, so that each has a unit).
+    template <int LEAST> static __device__ __forceinline__ Cut make(long long total, const FastDiv &most) {
+        Cut c;
+        c.total = total;
+        if (total < 0x40000000ll && (int)total >= LEAST * most.d) {      // nearly every call: no division
+            c.grid = most.d;
+            c.size = most.div((int)total);
+        } else {
+            c.grid = (int)min((long long)most.d, max(div_places(total, LEAST), 1ll));
+            c.size = div_places(total, c.grid);
+        }
+        c.longer = total - c.size * c.grid;
+        return c;
     }
     __device__ __forceinline__ long long begin(int c) const { return c * size + min((long long)c, longer); }
     __device__ __forceinline__ int owner(long long w) const {
@@ -144,7 +152,7 @@ __device__ __forceinline__ Cut find_range(const AttnArgs &p, Walk &walk, long lo
         incl += total;
         total = __shfl_sync(0xffffffffu, incl, 31);
     }
-    const Cut cut(total * p.c.n_kv, (int)gridDim.x, LEAST);
+    const Cut cut = Cut::make<LEAST>(total * p.c.n_kv, p.grid);
     first = last = 0;
     if (total == 0 || (int)blockIdx.x >= cut.grid) return cut;
     first = cut.begin(blockIdx.x);
@@ -185,12 +193,11 @@ struct Item {
     int r0, m, len, j, h;      // see UnitWalk
     int y0, n;                 // its units of this CTA: y0 .. y0 + n - 1; n == 0: no more items
     int rows, pos0, pos1, sinks, w0;
-    int c0, c1;                // CTAs that share it; c0 == c1: this one alone
+    int whole;                 // no other CTA has units of it
     int slot;                  // its part's place in the workspace
 };
 
-template <class Walk>
-__device__ __forceinline__ Item item_of(const Walk &at, const Cut &cut, long long first, long long last) {
+template <class Walk> __device__ __forceinline__ Item item_of(const Walk &at, long long first, long long last) {
     Item it;
     it.r0 = at.r0;
     it.m = at.m;
@@ -205,9 +212,7 @@ __device__ __forceinline__ Item item_of(const Walk &at, const Cut &cut, long lon
     it.w0 = at.t.w0;
     it.n = (int)min((long long)(at.t.units - at.y), last - at.w);
     const long long w0 = at.w - at.y, w1 = w0 + at.t.units - 1;      // places of its first and last unit
-    it.c0 = it.c1 = (int)blockIdx.x;
-    if (w0 < first) it.c0 = cut.owner(w0);
-    if (w1 >= last) it.c1 = cut.owner(w1);
+    it.whole = w0 >= first && w1 < last;
     it.slot = 2 * (int)blockIdx.x + (w0 < first ? 0 : 1);
     return it;
 }
@@ -221,6 +226,17 @@ struct Split {
 };
 __host__ __device__ constexpr size_t attn_splits_bytes() { return (kAttnMaxGrid * sizeof(Split) + 15) / 16 * 16; }
 __host__ __device__ constexpr size_t attn_part_floats(int rt, int d) { return (size_t)rt * (d + 2); }   // a multiple of 4 (rt is one of 8)
+// The item at `at` if it begins in this CTA (range [first, last)) and goes on.
+template <class Walk> __device__ __forceinline__ Split split_of(const Walk &at, const Cut &cut, long long first, long long last) {
+    const long long w0 = at.w - at.y, w1 = w0 + at.t.units - 1;
+    Split s;
+    s.c1 = w0 >= first && w1 >= last ? cut.owner(w1) : -1;
+    s.rows = at.t.rows;
+    s.r0 = at.r0;
+    s.j = at.j;
+    s.h = at.h;
+    return s;
+}
 __device__ __forceinline__ Split *splits_of(const AttnArgs &p) { return reinterpret_cast<Split *>(p.ws); }
 __device__ __forceinline__ float *parts_of(const AttnArgs &p) { return reinterpret_cast<float *>(p.ws + attn_splits_bytes()); }
 

@@ -185,8 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         Walk at;
         long long first, last;
         const Cut cut = find_range<Walk, kLeast>(p, at, first, last);
-        Split *split = splits_of(p) + blockIdx.x;
-        if (lane == 0) split->c1 = -1;
+        Split split;                       // of the last item: only that can go on in another CTA
+        split.c1 = -1;
+        if (lane == 0) splits_of(p)[blockIdx.x].c1 = -1;      // should a wait below run out
         uint32_t k = 0, n_unit = 0;
         bool fresh = true, dead = false;
         at.w = first == last ? last : at.w;
@@ -198,10 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fresh = false;
                     if (!mbar_wait(&i_empty[k % kItems], (k / kItems + 1) & 1u)) dead = true;
                     if (lane == 0 && !dead) {
-                        const Item it = item_of(at, cut, first, last);
-                        items[k % kItems] = it;
+                        items[k % kItems] = item_of(at, first, last);
                         mbar_arrive(&i_full[k % kItems]);
-                        if (it.c0 == (int)blockIdx.x && it.c1 > it.c0) *split = Split{it.c1, it.rows, it.r0, it.j, it.h};
                     }
                     ++k;
                 }
@@ -210,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     seq = at.s;
                     head = at.h;
                 }
+                if (at.w + 1 == last) split = split_of(at, cut, first, last);
                 if (at.y + 1 < at.t.units) {
                     ++at.y;
                     ++at.w;
@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        if (lane == 0) splits_of(p)[blockIdx.x] = split;
         if (!dead && !mbar_wait(&i_empty[k % kItems], (k / kItems + 1) & 1u)) dead = true;
         if (lane == 0 && !dead) {
             items[k % kItems].n = 0;
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 
             // ---------------- the item's end ----------------
-            const bool whole = it.c0 == it.c1;
+            const bool whole = it.whole;
             float *parts = parts_of(p);
             constexpr size_t PF = attn_part_floats(RT, D);
             T *out = static_cast<T *>(p.out) + (it.r0 + tok) * p.ldo + (long long)head * D;
@@ -667,7 +668,7 @@ template <class T, int D> cudaError_t launch(const AttnArgs &a, cudaStream_t s, 
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
     if (!make_map(&km, a.c.k, a.c) || !make_map(&vm, a.c.v, a.c)) return cudaErrorInvalidValue;
-    return launch_with_join<T, D, RT>(attn_tc<T, D>, (unsigned)(dev.sm_count < kTcGrid ? dev.sm_count : kTcGrid), kThreads, smem, km, vm, a, s);
+    return launch_with_join<T, D, RT>(attn_tc<T, D>, dev.sm_count < kTcGrid ? dev.sm_count : kTcGrid, kThreads, smem, km, vm, a, s);
 }
 
 }  // namespace

@@ -45,6 +45,7 @@ struct KvAppendArgs {
 struct AttnArgs {
     KvView c;
     FastDiv group;             // query heads per kv head
+    FastDiv grid;              // CTAs of the launch (set by the launcher)
     const void *q;
     void *out;
     long long ldq, ldo;
