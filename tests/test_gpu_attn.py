@@ -283,3 +283,86 @@ def test_no_rows(ws):
     assert pq.pq_attn(h, rs, 0, "f32", q, 64, 1, 1.0, 0, 0, out, 64, ws, ws.numel()) == 0
     torch.cuda.synchronize()
     assert torch.all(out == 1)
+
+
+def dense64(t, c, q, n_q, pos, window=0, sinks=0):
+    """64-bit attention of the rows of one sequence on the GPU; returns (out, max|v|)."""
+    import torch
+    n = int(c.len[0])
+    tok = torch.arange(n, device="cuda")
+    pg = t["table"][0, tok // c.page].long()
+    hide = tok > pos[:, None]
+    if window:
+        hide = hide | ((pos[:, None] - tok >= window) & (tok >= sinks))
+    out = torch.empty(q.shape[0], n_q, c.d, dtype=torch.float64, device="cuda")
+    vmax = 0.0
+    for h in range(c.n_kv):
+        k = t["k"][pg, h, tok % c.page].double() * t["ks"][pg, h].double()[:, None]
+        v = t["v"][pg, h, tok % c.page].double() * t["vs"][pg, h].double()[:, None]
+        vmax = max(vmax, float(v.abs().max()))
+        for j in range(h * n_q // c.n_kv, (h + 1) * n_q // c.n_kv):
+            x = (q.double()[:, j] @ k.T * float(np.float32(c.d ** -0.5))).masked_fill(hide, -float("inf"))
+            out[:, j] = torch.softmax(x, -1) @ v
+    return out, vmax
+
+
+@pytest.mark.parametrize("dt,rows,n,heads,window,sinks", [
+    ("bf16", 1, 25001, (32, 8, 128), 0, 0), ("f16", 1, 30000, (14, 2, 64), 0, 0), ("f32", 1, 20011, (16, 1, 64), 0, 0),
+    ("f32", 9, 9000, (8, 2, 128), 0, 0), ("bf16", 700, 3100, (32, 8, 128), 0, 0), ("f16", 1500, 1500, (14, 2, 64), 0, 0),
+    ("bf16", 64, 30000, (8, 1, 128), 0, 0), ("f16", 900, 5000, (8, 2, 128), 500, 130), ("bf16", 9, 50000, (32, 8, 128), 20000, 7),
+])
+def test_long_contexts(dt, rows, n, heads, window, sinks, ws):
+    import torch
+    n_q, n_kv, d = heads
+    c = kvref.Cache(1, [n], n_kv, 64, d, seed=rows)
+    t, h = upload(c)
+    q = torch.randn(rows, n_q * d, device="cuda", generator=torch.Generator("cuda").manual_seed(rows)).to(tdt(dt))
+    out = torch.empty_like(q)
+    rs = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    ws.fill_(0xA5)                                    # what the workspace holds does not matter
+    pq.pq_attn(h, rs, rows, dt, q, n_q * d, n_q, d ** -0.5, window, sinks, out, n_q * d, ws, ws.numel())
+    pos = torch.arange(n - rows, n, device="cuda")
+    ref, vmax = dense64(t, c, q.view(rows, n_q, d), n_q, pos, window, sinks)
+    u = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dt]
+    tol = (4e-5 + (2.0 ** -11 if dt != "f32" else 0.0)) * vmax + u * ref.abs()
+    assert bool(((out.double().view_as(ref) - ref).abs() <= tol).all())
+    # by the mean square: below the formats' own rounding by half again, f32 below 2e-6
+    rel = float((out.double().view_as(ref) - ref).norm() / ref.norm())
+    assert rel <= {"f32": 2e-6, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dt]
+
+
+@pytest.mark.parametrize("window,sinks", [(5, 0), (64, 9), (300, 33)])
+def test_window_at_other_head_sizes(window, sinks, ws):
+    c = kvref.Cache(3, [90, 300, 1], 2, 16, 80, seed=window)
+    check(*run(c, [3, 40, 1], "f32", 6, ws, window=window, sinks=sinks), "f32")
+
+
+def test_two_streams_with_a_workspace_each(ws):
+    import torch
+    c = [kvref.Cache(1, [3000], 8, 64, 128, seed=40 + i) for i in range(2)]
+    up = [upload(x) for x in c]
+    q = [torch.randn(1, 32 * 128, device="cuda") for _ in range(2)]
+    alone, both = ([torch.empty_like(x) for x in q] for _ in range(2))
+    size = pq.pq_attn_ws_bytes(32, 8, 128)
+    spaces = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for i in range(2):
+        pq.pq_attn(up[i][1], None, 1, "f32", q[i], 4096, 32, 0.088, 0, 0, alone[i], 4096, ws, ws.numel())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for i in range(2):
+            pq.pq_attn(up[i][1], None, 1, "f32", q[i], 4096, 32, 0.088, 0, 0, both[i], 4096, spaces[i], size, stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(alone[i], both[i])
+
+
+def test_the_last_rows_of_a_token_split_over_row_tiles(ws):
+    # 14 query heads per kv head: row tiles of 8, 16 and 256 rows end inside a token
+    for dt, news in (("f32", [3, 1]), ("bf16", [2, 2]), ("f16", [41, 19])):
+        c = kvref.Cache(2, [200, 133], 1, 32, 64, seed=51)
+        check(*run(c, news, dt, 14, ws), dt)
+
+
+def test_no_wait_ran_out():
+    assert pq.pq_wait_timeouts() == 0
