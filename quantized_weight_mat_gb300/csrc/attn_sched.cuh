@@ -18,7 +18,9 @@
 
 namespace pqk {
 
-constexpr int kAttnMaxGrid = 320;      // CTAs at most (parts and counters in the workspace)
+constexpr int kAttnMaxGrid = 320;      // CTAs at most (parts in the workspace)
+
+constexpr int kFewTiles = 4;           // a sequence's row tiles that one lane counts by itself
 
 // One row tile: its rows, the positions they cover, the token tiles they see.
 struct RowTile {
@@ -90,18 +92,42 @@ template <int RT, int KT, int COST> struct UnitWalk {
     // Places of one kv head of the sequence.
     __device__ __forceinline__ long long places(const AttnArgs &p) const {
         long long n = 0;
-        for (int i = 0; i < tiles; ++i) n += row_tile<RT, KT>(p, m, len, i).units + COST;
+        for (int i = 0; i < tiles; ++i) n += tile_places(p, i);
         return n;
     }
-    // The first unit at place `first` or after it, which lies `x` into the
+    __device__ __forceinline__ int tile_places(const AttnArgs &p, int i) const { return row_tile<RT, KT>(p, m, len, i).units + COST; }
+    // By one warp: the first unit at place `first` or after it, which lies `x` into the
     // sequence, of `per_head` places per kv head.
     __device__ __forceinline__ void start(const AttnArgs &p, long long first, long long x, long long per_head) {
         h = (int)div_places(x, per_head);
         long long left = x - h * per_head;
-        for (j = 0;; ++j) {
+        j = 0;
+        if (tiles > kFewTiles) {      // 32 row tiles at a time, one per lane
+            const int lane = threadIdx.x & 31;
+            for (;; j += 32) {
+                const int n = j + lane < tiles ? row_tile<RT, KT>(p, m, len, j + lane).units + COST : 0;
+                int incl = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, left < incl);
+                const int at = hit ? __ffs((int)hit) - 1 : 31;
+                left -= __shfl_sync(0xffffffffu, hit ? incl - n : incl, at);
+                if (hit) {
+                    j += at;
+                    break;
+                }
+                if (j + 32 >= tiles) break;      // not reached: the places end in the sequence
+            }
             t = row_tile<RT, KT>(p, m, len, j);
-            if (left < t.units + COST) break;
-            left -= t.units + COST;
+        } else {
+            for (;; ++j) {
+                t = row_tile<RT, KT>(p, m, len, j);
+                if (left < t.units + COST) break;
+                left -= t.units + COST;
+            }
         }
         y = max(0, (int)left - COST);
         w = first + y + COST - left;
@@ -131,7 +157,21 @@ template <class Walk> __device__ __forceinline__ long long warp_places(const Att
     walk.s = s + lane;
     walk.m = 0;
     if (walk.s < p.c.n_seq) walk.seq(p);
-    return walk.m > 0 ? walk.places(p) : 0;
+    const int tiles = walk.m > 0 ? walk.tiles : 0;
+    long long n = tiles > 0 && tiles <= kFewTiles ? walk.places(p) : 0;
+    // sequences of many row tiles one after the other, by all lanes
+    for (unsigned many = __ballot_sync(0xffffffffu, tiles > kFewTiles); many; many &= many - 1) {
+        const int src = __ffs((int)many) - 1, count = __shfl_sync(0xffffffffu, tiles, src);
+        Walk of = walk;
+        of.m = __shfl_sync(0xffffffffu, walk.m, src);
+        of.len = __shfl_sync(0xffffffffu, walk.len, src);
+        long long sum = 0;
+        for (int i = lane; i < count; i += 32) sum += of.tile_places(p, i);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == src) n = sum;
+    }
+    return n;
 }
 
 // By one warp: the places of the call, cut into ranges of at least LEAST, and

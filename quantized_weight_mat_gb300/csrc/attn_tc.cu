@@ -35,6 +35,8 @@
 // and takes those columns again.  Tiles at an edge of some row's view, or with
 // page scales that are no ordinary positive numbers, take a masking variant.
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "pq_tcgen05.cuh"
 
@@ -45,14 +47,18 @@ constexpr int RT = 256, HALF = 128;          // rows of an item, and of each hal
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kWalkWarp = kSoftmaxWarps + kConvertWarps, kMmaWarp = kWalkWarp + 1, kScaleWarp = kWalkWarp + 2;
 constexpr int kThreads = 32 * (kScaleWarp + 1);
-constexpr int kRaw = 3, kMeta = 4, kItems = 8, kItemCost = 2;
+constexpr int kImages = 3, kMeta = 4, kItems = 8, kItemCost = 2;
 constexpr int kLeast = 4;                    // places of a CTA
 constexpr int kTcGrid = 160;                 // CTAs at most: one per SM
 constexpr int kTmemCols = 512;
+constexpr float kMost = 32768.f;             // the running maximum moves when a row's weights of one step sum to more: fp16 holds each
+constexpr float kFar = 1048576.f;            // maxima up to here leave room for the V scales beside them
 using Walk = UnitWalk<RT, KT, kItemCost>;
 
+// raw tiles, K and V in turn
+template <int D> __host__ __device__ constexpr int raw_tiles() { return D == 128 ? 4 : 8; }
 template <int D> __host__ __device__ constexpr int smem_bytes() {
-    return 1024 + RT * D * 2 + 2 * KT * D * 2 + kRaw * 2 * KT * D;
+    return 1024 + RT * D * 2 + kImages * KT * D * 2 + raw_tiles<D>() * KT * D;
 }
 static_assert(smem_bytes<128>() <= 226 * 1024, "shared memory per CTA, beside the static part");
 
@@ -83,12 +89,6 @@ __device__ __forceinline__ void add2(float &sx, float &sy, float x, float y) {
         : "f"(x), "f"(y));
 }
 
-__device__ __forceinline__ float max3(uint32_t x, uint32_t y, uint32_t z) {
-    float m;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(x)), "f"(__uint_as_float(y)), "f"(__uint_as_float(z)));
-    return m;
-}
-
 // A tile's page scales as the softmax takes them.
 struct TileScales {
     float ks[kGroups], vs[kGroups], lv[kGroups];      // lv = log2(vs)
@@ -97,6 +97,8 @@ struct TileScales {
     int ve_max;
     int have;                                         // bit g: group g has a page
     int plain;                                        // bit g: it does, with ordinary positive scales
+    int t0;                                           // its first token
+    bool quick;                                       // all groups plain, the V scales within 2^58 of each other
 };
 
 // One tile of codes (128 tokens, swizzled as TMA left it) to its fp16 image, by the four converting warps.
@@ -126,17 +128,18 @@ template <class T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs p) {
     constexpr uint32_t ID_S = instr_desc(HALF, KT), ID_O = instr_desc(HALF, D) | (1u << 16);      // bit 16: B is MN-major
+    constexpr int kRaw = raw_tiles<D>();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], meta_full[kMeta], meta_empty[kMeta], scales_full[kMeta], i_full[kItems],
-        i_empty[kItems], k_ready, k_free, v_ready, v_free, s_full[2], p_ready[2], pv_done[2], q_ready;
+        i_empty[kItems], image_full[kImages], image_empty[kImages], s_full[2], p_ready[2], pv_done[2], q_ready;
     __shared__ __align__(16) TileMeta meta[kMeta];
     __shared__ __align__(16) TileScales scales[kMeta];
     __shared__ Item items[kItems];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int stop, stop_convert;
 
-    // converted V and K, q, raw tiles, from a 1024-byte boundary
-    const uint32_t v0 = (smem_u32(smem_raw) + 1023u) & ~1023u, k0 = v0 + KT * D * 2, q0 = k0 + KT * D * 2, raw0 = q0 + RT * D * 2;
+    // converted tiles, q, raw tiles, from a 1024-byte boundary; of both kinds of tile, K of unit u is number 2 u and V 2 u + 1
+    const uint32_t image0 = (smem_u32(smem_raw) + 1023u) & ~1023u, q0 = image0 + kImages * KT * D * 2, raw0 = q0 + RT * D * 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         stop = stop_convert = 0;
@@ -153,10 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&i_full[i], 1);
             mbar_init(&i_empty[i], 4);
         }
-        mbar_init(&k_ready, kConvertWarps);
-        mbar_init(&k_free, 1);
-        mbar_init(&v_ready, kConvertWarps);
-        mbar_init(&v_free, 1);
+        for (int i = 0; i < kImages; ++i) {
+            mbar_init(&image_full[i], kConvertWarps);
+            mbar_init(&image_empty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 4);
@@ -220,30 +223,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int pg = sub < n ? page_of(p.c, seq, tok / p.c.page) : -1;
             for (int i = 0; i < n && !dead; ++i, ++n_unit) {
-                const int slot = n_unit % kRaw, ms = n_unit % kMeta;
-                if (!mbar_wait(&meta_empty[ms], (n_unit / kMeta + 1) & 1u) || !mbar_wait(&raw_empty[slot], (n_unit / kRaw + 1) & 1u)) {
+                const int ms = n_unit % kMeta;
+                if (!mbar_wait(&meta_empty[ms], (n_unit / kMeta + 1) & 1u)) {
                     dead = true;
                     break;
                 }
                 if (sub == i) meta[ms].have[g] = pg >= 0;
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&meta_full[ms]);
-                    mbar_arrive_expect_tx(&raw_full[slot], 2 * KT * D);
-                }
+                if (lane == 0) mbar_arrive(&meta_full[ms]);
                 __syncwarp();
                 if (sub == i) {
-                    if (16 * g % p.c.page == 0) {
-                        // no page: a box outside the tensor, which reads as zeros
-                        const int row = head * p.c.page + tok % p.c.page, z = pg >= 0 ? pg : p.c.n_pages;
-                        const uint32_t dst = raw0 + slot * 2 * KT * D + 16 * g * D;
-                        tma_load_3d(dst, &kmap, 0, row, z, &raw_full[slot]);
-                        tma_load_3d(dst + KT * D, &vmap, 0, row, z, &raw_full[slot]);
-                    }
                     const long long si = pg >= 0 ? (long long)pg * p.c.n_kv + head : 0;
                     copy4(&meta[ms].ks[g], p.c.k_scale + si, pg >= 0);
                     copy4(&meta[ms].vs[g], p.c.v_scale + si, pg >= 0);
                     copies_arrive(&meta_full[ms]);
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t j = 2 * n_unit + kv, slot = j % kRaw;
+                    if (dead || !mbar_wait(&raw_empty[slot], (j / kRaw + 1) & 1u)) {
+                        dead = true;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], KT * D);
+                    __syncwarp();
+                    if (sub == i && 16 * g % p.c.page == 0) {
+                        // no page: a box outside the tensor, which reads as zeros
+                        const int row = head * p.c.page + tok % p.c.page, z = pg >= 0 ? pg : p.c.n_pages;
+                        tma_load_3d(raw0 + slot * KT * D + 16 * g * D, kv ? &vmap : &kmap, 0, row, z, &raw_full[slot]);
+                    }
                 }
             }
         }
@@ -253,58 +261,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             items[k % kItems].n = 0;
             mbar_arrive(&i_full[k % kItems]);
         }
-        } else if (warp == kMmaWarp && lane == 0) {
-        // ---------------- products ----------------
+        } else if (warp == kMmaWarp) {
+        // ---------------- products (the whole warp, one lane issuing) ----------------
+            const uint32_t one = elect_one(), tm = __reduce_max_sync(0xffffffffu, tmem);
             uint32_t units = 0, parity[2] = {0u, 0u};
-            const uint64_t kd = smem_desc(k0, 128u, 16u * D), vd = smem_desc(v0, 16u * D, 128u);
-            uint64_t qd[2];
+            const uint64_t kd = smem_desc(image0, 128u, 16u * D), vd = smem_desc(image0, 16u * D, 128u), qd = smem_desc(q0, 128u, 16u * D);
+            auto wait = [](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+            auto image = [](uint32_t j) { return (uint64_t)(j % kImages * (KT * D * 2 / 16)); };
+            auto filled = [&](uint32_t j) { return wait(&image_full[j % kImages], (j / kImages) & 1u); };
+            auto scores = [&](int h, uint32_t u) {
+                const uint64_t a = qd + (uint64_t)(h * (HALF * D * 2 / 16)), b = kd + image(2 * u);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) qd[h] = smem_desc(q0 + h * HALF * D * 2, 128u, 16u * D);
-            auto scores = [&](int h) {
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) mma_f16(tmem + 128u * h, qd[h] + 16u * c, kd + 16u * c, ID_S, c > 0);
-                mma_commit(&s_full[h]);
+                for (int c = 0; c < D / 16; ++c) mma_f16_one(one, tm + 128u * h, a + 16u * c, b + 16u * c, ID_S, c > 0);
+                mma_commit_one(one, &s_full[h]);
             };
-            auto outputs = [&](int h, bool add) {
+            auto outputs = [&](int h, uint32_t u, bool add) {
+                const uint64_t b = vd + image(2 * u + 1);
 #pragma unroll
                 for (int c = 0; c < KT / 16; ++c)
-                    mma_f16_ta(tmem + 256u + 128u * h, tmem + 128u * h + 8u * c, vd + (uint64_t)(2 * D * c), ID_O, add || c > 0);
-                mma_commit(&pv_done[h]);
+                    mma_f16_ta_one(one, tm + 256u + 128u * h, tm + 128u * h + 8u * c, b + (uint64_t)(2 * D * c), ID_O, add || c > 0);
+                mma_commit_one(one, &pv_done[h]);
             };
             bool dead = false;
             for (uint32_t k = 0; !dead; ++k) {
-                if (!mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) break;
-                const int n = items[k % kItems].n, halves = items[k % kItems].rows > HALF ? 2 : 1;
+                if (!wait(&i_full[k % kItems], (k / kItems) & 1u)) break;
+                const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)items[k % kItems].n);
+                const int halves = __any_sync(0xffffffffu, items[k % kItems].rows > HALF) ? 2 : 1;
                 if (n == 0) break;
-                mbar_arrive(&i_empty[k % kItems]);
-                if (!mbar_wait(&q_ready, k & 1u) || !mbar_wait(&k_ready, units & 1u)) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&i_empty[k % kItems]);
+                if (!wait(&q_ready, k & 1u) || !filled(2 * units)) break;
                 tc_fence_after();
-                scores(0);
-                if (halves == 2) scores(1);
-                mma_commit(&k_free);
+                scores(0, units);
+                if (halves == 2) scores(1, units);
+                mma_commit_one(one, &image_empty[2 * units % kImages]);
                 for (int i = 0; i < n && !dead; ++i, ++units) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (dead || h == halves) break;
                         // P V of this tile, then S of the next one over the same columns
-                        if ((h == 0 && !mbar_wait(&v_ready, units & 1u)) || !mbar_wait(&p_ready[h], parity[h])) {
+                        if ((h == 0 && !filled(2 * units + 1)) || !wait(&p_ready[h], parity[h])) {
                             dead = true;
                             break;
                         }
                         parity[h] ^= 1u;
                         tc_fence_after();
-                        outputs(h, i > 0);
-                        if (h == halves - 1) mma_commit(&v_free);
+                        outputs(h, units, i > 0);
+                        if (h == halves - 1) mma_commit_one(one, &image_empty[(2 * units + 1) % kImages]);
                         if (i + 1 < n) {
                             if (h == 0) {
-                                if (!mbar_wait(&k_ready, (units + 1) & 1u)) {
+                                if (!filled(2 * units + 2)) {
                                     dead = true;
                                     break;
                                 }
                                 tc_fence_after();
                             }
-                            scores(h);
-                            if (h == halves - 1) mma_commit(&k_free);
+                            scores(h, units + 1);
+                            if (h == halves - 1) mma_commit_one(one, &image_empty[(2 * units + 2) % kImages]);
                         }
                     }
                 }
@@ -316,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool dead = false;
             for (uint32_t k = 0; !dead; ++k) {
                 if (!mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) break;
-                const int n = items[k % kItems].n;
+                const int n = items[k % kItems].n, y0 = items[k % kItems].y0, sinks = items[k % kItems].sinks, w0 = items[k % kItems].w0;
                 __syncwarp();
                 if (n == 0) break;
                 if (lane == 0) mbar_arrive(&i_empty[k % kItems]);
@@ -350,6 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ts.ve_max = ve_max;
                         ts.have = (int)(haves & 0xffu);
                         ts.plain = (int)(plains & 0xffu);
+                        ts.t0 = (y0 + i < sinks ? y0 + i : w0 + (y0 + i - sinks)) * KT;
+                        ts.quick = p.scale >= 0.f && (plains & 0xffu) == 0xffu && lv_min - (float)ve_max > -58.f;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&scales_full[ms]);
@@ -370,20 +385,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_sync(2, 32 * kConvertWarps);
             if (cw == 0 && lane == 0) mbar_arrive(&i_empty[k % kItems]);
             for (int i = 0; i < n; ++i, ++unit) {
-                const int slot = unit % kRaw;
-                const uint32_t raw = raw0 + slot * 2 * KT * D;
-                if (!dead && (!mbar_wait(&raw_full[slot], (unit / kRaw) & 1u) || !mbar_wait(&k_free, (unit + 1) & 1u))) dead = true;
-                convert_tile<D>(raw, k0, cw, lane);
-                proxy_fence();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&k_ready);
-                if (!dead && !mbar_wait(&v_free, (unit + 1) & 1u)) dead = true;
-                convert_tile<D>(raw + KT * D, v0, cw, lane);
-                proxy_fence();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&v_ready);
-                    mbar_arrive(&raw_empty[slot]);
+#pragma unroll 1
+                for (uint32_t j = 2 * unit; j < 2 * unit + 2; ++j) {
+                    const uint32_t slot = j % kRaw, im = j % kImages;
+                    if (!dead && (!mbar_wait(&raw_full[slot], (j / kRaw) & 1u) || !mbar_wait(&image_empty[im], (j / kImages + 1) & 1u))) dead = true;
+                    convert_tile<D>(raw0 + slot * KT * D, image0 + im * KT * D * 2, cw, lane);
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&image_full[im]);
+                        mbar_arrive(&raw_empty[slot]);
+                    }
                 }
             }
         }
@@ -394,41 +406,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + 128u * half + lanes, to = tmem + 256u + 128u * half + lanes;
         uint32_t unit = 0, tiles = 0;                     // units of the CTA, and those with this half
         bool dead = false;
+        // rows of q come in and rows of the output leave through the 32 rows' part of the q image, 16 bytes a lane,
+        // CH lanes a row, so that global memory sees whole rows
+        constexpr int CH = D / 8, ROWS = 32 / CH;
+        const int sub = lane / CH, ch = lane % CH, row0 = HALF * half + 32 * (warp & 3);
+        const uint32_t stage = q0 + row0 * D * 2;
         for (uint32_t k = 0;; ++k) {
             if (!mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) stop = 1;
             named_sync(1, 32 * kSoftmaxWarps);            // every warp leaves here, or none
             const Item &it = items[k % kItems];           // this group's until it says so below
             if (stop || it.n == 0) break;
             const bool act = it.rows > HALF * half;
-            const int r = HALF * half + 32 * (warp & 3) + lane;
+            const int r = row0 + lane;
             const bool have = r < it.rows;
             const int tok = p.group.div(it.j * RT + r), head = it.h * p.group.d + it.j * RT + r - tok * p.group.d;
             const int pos = have ? it.len - it.m + tok : -1;
             float fac = 0.f;
             if (act) {
                 // the row of q: power-of-two scale, fp16, operand image
-                const T *src = static_cast<const T *>(p.q) + (it.r0 + tok) * p.ldq + (long long)head * D;
-                uint32_t top = 0;
+                const T *mine = static_cast<const T *>(p.q) + (it.r0 + tok) * p.ldq + (long long)head * D;
+                uint4 w[CH];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    float x[8];
-                    if (have) load8(src + 8 * c, x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = max(top, have ? __float_as_uint(x[e]) & 0x7fffffffu : 0u);
+                for (int i = 0; i < CH; ++i) {
+                    const int src = i * ROWS + sub;
+                    const T *row = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), src));
+                    w[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (row0 + src < it.rows) w[i] = *(reinterpret_cast<const uint4 *>(row) + ch);
                 }
-                const int ex = tc_scale_exponent(top);
-                const float up = pow2(ex);
+                uint32_t of_mine = 0;
+#pragma unroll
+                for (int i0 = 0; i0 < CH; i0 += 8) {
+                    uint32_t top[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float x[8];
+                        load8(reinterpret_cast<const T *>(&w[i0 + i]), x);
+                        top[i] = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top[i] = max(top[i], __float_as_uint(x[e]) & 0x7fffffffu);
+                    }
+#pragma unroll
+                    for (int o = 1; o < CH; o <<= 1)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t t = __shfl_sync(0xffffffffu, top[i], lane % ROWS * CH);
+                        if (lane / ROWS == i0 + i) of_mine = t;
+                        float x[8];
+                        load8(reinterpret_cast<const T *>(&w[i0 + i]), x);
+                        const float up = pow2(tc_scale_exponent(top[i]));
+                        sts128(stage + image_at<D>((i0 + i) * ROWS + sub, ch),
+                               make_uint4(pack2(x[0] * up, x[1] * up), pack2(x[2] * up, x[3] * up), pack2(x[4] * up, x[5] * up),
+                                          pack2(x[6] * up, x[7] * up)));
+                    }
+                }
+                const int ex = tc_scale_exponent(of_mine);
                 fac = pow2(-ex) * (p.scale * kLog2e);
-                const uint32_t dst = q0 + half * HALF * D * 2;
-                // (read again: the row would not fit beside what the loop below keeps)
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    if (have) load8(src + 8 * c, x);
-                    sts128(dst + image_at<D>(r - HALF * half, c),
-                           make_uint4(pack2(x[0] * up, x[1] * up), pack2(x[2] * up, x[3] * up), pack2(x[4] * up, x[5] * up),
-                                      pack2(x[6] * up, x[7] * up)));
-                }
                 proxy_fence();
             }
             __syncwarp();
@@ -436,26 +470,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             float m = -INFINITY, l = 0.f;
             int vexp = kMinExp;
-            for (int y = it.y0; y < it.y0 + it.n; ++y, ++unit) {
+            const int n = it.n;
+            for (int i = 0; i < n; ++i, ++unit) {
                 const TileScales &sc = scales[unit % kMeta];
                 if (!dead && !mbar_wait(&scales_full[unit % kMeta], (unit / kMeta) & 1u)) dead = true;
                 if (act) {
-                    const int t0 = (y < it.sinks ? y : it.w0 + (y - it.sinks)) * KT;
-                    // the row sees the tile's tokens e with e <= to_pos and (e > to_window or e < to_sink)
-                    const int to_pos = pos - t0, to_window = p.window > 0 ? pos - p.window - t0 : -1, to_sink = p.n_sink - t0;
-                    const bool whole_view = !have || (to_pos >= KT - 1 && (to_window < 0 || to_sink >= KT));
-                    // V scales in the exponent: at most 2^60 below the reference, which may move to ve_max + 2
-                    const bool near = p.scale >= 0.f && __all_sync(0xffffffffu, !have || sc.lv_min - (float)max(vexp, sc.ve_max + 2) > -60.f);
-                    const bool all = near && __all_sync(0xffffffffu, whole_view) && sc.plain == (1 << kGroups) - 1;
-                    // which of the tokens 32c .. 32c + 31 the row sees
+                    // the row sees the tile's tokens e with e <= last and (e >= first or e < sink): all of them,
+                    auto whole_view = [&] {
+                        const int last = pos - sc.t0, first = p.window > 0 ? last - p.window + 1 : 0, sink = p.n_sink - sc.t0;
+                        return last >= KT - 1 && (first <= 0 || sink >= KT);
+                    };
+                    // and which of 32 c .. 32 c + 31
                     auto view = [&](int c) {
                         auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+                        const int last = pos - sc.t0, first = p.window > 0 ? last - p.window + 1 : 0, sink = p.n_sink - sc.t0;
                         const uint32_t pages = ((sc.have >> (2 * c)) & 1 ? 0xffffu : 0u) | ((sc.have >> (2 * c + 1)) & 1 ? 0xffff0000u : 0u);
-                        return pages & below(to_pos + 1 - 32 * c) & (~below(to_window + 1 - 32 * c) | below(to_sink - 32 * c));
+                        return pages & below(last + 1 - 32 * c) & (~below(first - 32 * c) | below(sink - 32 * c));
                     };
                     // O of the tiles before this one, times the row's a
                     auto rescale = [&](float a) {
-                        if (y == it.y0) return;
+                        if (i == 0) return;
                         if (!dead && !mbar_wait(&pv_done[half], (tiles + 1) & 1u)) dead = true;
                         tc_fence_after();
 #pragma unroll 1
@@ -469,29 +503,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_st_wait();
                     };
-                    // ---- the V scales' reference
-                    int big = kMinExp;
-                    if (all) {
-                        if (have) big = sc.ve_max;
-                    } else if (__any_sync(0xffffffffu, sc.ve_max > vexp)) {
+                    // ---- the V scales' reference; mostly all rows see the whole tile and nothing moves
+                    bool near = true, all = true;
+                    const bool quick = __all_sync(0xffffffffu, sc.quick && (!have || (whole_view() && fabsf(m) < kFar && sc.ve_max <= vexp && sc.lv_min - (float)vexp > -60.f)));
+                    if (__builtin_expect(!quick, 0)) {
+                        // V scales in the exponent: at most 2^60 below the reference, which may move to ve_max + 2, and beside
+                        // a maximum whose last bit does not swallow them
+                        near = p.scale >= 0.f && __all_sync(0xffffffffu, !have || ((fabsf(m) < kFar || m == -INFINITY) && sc.lv_min - (float)max(vexp, sc.ve_max + 2) > -60.f));
+                        all = near && sc.plain == (1 << kGroups) - 1;
+                        int big = kMinExp;
+                        if (__any_sync(0xffffffffu, sc.ve_max > vexp)) {
 #pragma unroll 1
-                        for (int g = 0; g < kGroups; ++g)
-                            if (((sc.have >> g) & 1) && 16 * g <= to_pos && (min(16 * g + 15, to_pos) > to_window || 16 * g < to_sink))
-                                big = max(big, sc.ve[g]);
-                    }
-                    if (__any_sync(0xffffffffu, big > vexp)) {
-                        float a = 1.f;
-                        if (big > vexp) {
-                            big += 2;                 // room to grow
-                            a = vexp == kMinExp ? 0.f : pow2(vexp - big);
-                            vexp = big;
+                            for (int c = 0; c < KT / 32; ++c) {
+                                const uint32_t bits = view(c);
+                                if (bits & 0xffffu) big = max(big, sc.ve[2 * c]);
+                                if (bits >> 16) big = max(big, sc.ve[2 * c + 1]);
+                            }
                         }
-                        rescale(a);
+                        if (__any_sync(0xffffffffu, big > vexp)) {
+                            float a = 1.f;
+                            if (big > vexp) {
+                                big += 2;                 // room to grow
+                                a = vexp == kMinExp ? 0.f : pow2(vexp - big);
+                                vexp = big;
+                            }
+                            rescale(a);
+                        }
                     }
                     if (!dead && !mbar_wait(&s_full[half], tiles & 1u)) dead = true;
                     tc_fence_after();
-                    // the row's maximum moves to `top` if that is larger, with c times 16 columns of P in place
-                    auto raise = [&](int c, float top) {
+                    // the row's maximum moves to the largest score that it sees (bits) of the n steps from c, if that is
+                    // larger; the weights of the steps before are in place
+                    auto raise = [&](int c, int n, unsigned long long bits) {
+                        float top = -INFINITY;
+                        tmem_st_wait();
+#pragma unroll 1
+                        for (int g = 2 * c; g < 2 * (c + n); ++g, bits >>= 16) {
+                            uint32_t x[16];
+                            tmem_ld16(ts + 16 * g, x);
+                            tmem_ld_wait(x);
+                            const float f = sc.ks[g] * fac;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if ((bits >> e) & 1) top = fmaxf(top, __fmul_rn(__uint_as_float(x[e]), f));
+                        }
                         float a = 1.f;
                         if (top > m) {
                             a = m == -INFINITY ? 0.f : ex2(m - top);
@@ -503,7 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int i = 0; i < c; ++i) {
                             uint32_t w[16];
-                            tmem_st_wait();
                             tmem_ld16(ts + 16 * i, w);
                             tmem_ld_wait(w);
 #pragma unroll
@@ -514,98 +568,114 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st16(ts + 16 * i, w);
                         }
                     };
-                    if (all) {
-#pragma unroll 1
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t out[32];
-                            float add;
-                            for (;;) {
-                                uint32_t s[2][32];
-                                tmem_ld32(ts + 64 * c, s[0]);
-                                tmem_ld32(ts + 64 * c + 32, s[1]);
-                                tmem_ld_wait(s[0]);
-                                tmem_ld_wait(s[1]);
-                                const float base = m == -INFINITY ? 0.f : m;
-                                float top = -INFINITY;
-                                add = 0.f;
+                    int done = 0;                             // steps of 32 columns
+                    // weights of the 64 tokens from step done, of those in b0 and b1 if MASK: fp16 pairs, and their sum
+                    uint32_t out[32];
+                    auto weights = [&](auto mask, uint32_t b0, uint32_t b1) {
+                        constexpr bool MASK = decltype(mask)::value;
+                        uint32_t x[2][16];
+                        float add = 0.f;
+                        tmem_ld16(ts + 32 * done, x[0]);
 #pragma unroll
-                                for (int gi = 0; gi < 4; ++gi) {
-                                    const float f = sc.ks[4 * c + gi] * fac, lr = sc.lv[4 * c + gi] - (float)vexp;
-                                    uint32_t *x = &s[gi >> 1][16 * (gi & 1)];
+                        for (int g = 0; g < 4; ++g) {
+                            const float f = sc.ks[2 * done + g] * fac, lr = sc.lv[2 * done + g] - (float)vexp, c = have ? lr - m : -INFINITY, undo = ex2(-lr);
+                            uint32_t(&s)[16] = x[g & 1];
+                            tmem_ld_wait(s);
+                            if (g < 3) tmem_ld16(ts + 32 * done + 16 * (g + 1), x[(g + 1) & 1]);
+                            float sx = 0.f, sy = 0.f;
 #pragma unroll
-                                    for (int e = 0; e < 16; e += 2) fma2(x[e], x[e + 1], f, lr - base);
-                                    float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]);
-#pragma unroll
-                                    for (int e = 6; e < 14; e += 4) {
-                                        a = max3(__float_as_uint(a), x[e], x[e + 1]);
-                                        b = max3(__float_as_uint(b), x[e + 2], x[e + 3]);
-                                    }
-                                    a = max3(__float_as_uint(a), x[14], x[15]);
-                                    top = fmaxf(top, fmaxf(a, b) - lr);
-                                    float sx = 0.f, sy = 0.f;
-#pragma unroll
-                                    for (int e = 0; e < 16; e += 2) {
-                                        const float wx = ex2(__uint_as_float(x[e])), wy = ex2(__uint_as_float(x[e + 1]));
-                                        add2(sx, sy, wx, wy);
-                                        out[8 * gi + e / 2] = pack2(wx, wy);
-                                    }
-                                    add = fmaf(sx + sy, ex2(-lr), add);
+                            for (int e = 0; e < 16; e += 2) {
+                                fma2(s[e], s[e + 1], f, c);
+                                if (MASK) {
+                                    const uint32_t b = (g < 2 ? b0 : b1) >> (16 * (g & 1) + e);
+                                    if (!(b & 1)) s[e] = 0xff800000u;
+                                    if (!(b & 2)) s[e + 1] = 0xff800000u;
                                 }
-                                // the maximum is passed by more than its lag, or there is none yet: move it, and again
-                                if (!__any_sync(0xffffffffu, top > kSlack || (m == -INFINITY && top > -INFINITY))) break;
-                                raise(2 * c, top + base);
+                                const float wx = ex2(__uint_as_float(s[e])), wy = ex2(__uint_as_float(s[e + 1]));
+                                add2(sx, sy, wx, wy);
+                                out[8 * g + e / 2] = pack2(wx, wy);
                             }
-                            l += add;
-                            tmem_st32(ts + 32 * c, out);      // over columns of S that have been read
+                            add = fmaf(sx + sy, undo, add);
                         }
-                    } else {
-                        // the same at an edge of some row's view, or with other scales
-                        const unsigned plain = near ? (unsigned)sc.plain : 0u;
+                        return add;
+                    };
+                    bool go = quick;
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t out[16];
-                            const uint32_t bits = view(c);
-                            float add;
-                            for (;;) {
-                                uint32_t x[32];
-                                tmem_ld32(ts + 32 * c, x);
-                                tmem_ld_wait(x);
-                                const float base = m == -INFINITY ? 0.f : m;
-                                float top = -INFINITY;
-                                add = 0.f;
-#pragma unroll
-                                for (int gi = 0; gi < 2; ++gi) {
-                                    const int g = 2 * c + gi;
-                                    const bool in = (plain >> g) & 1;      // the V scale is in the exponent
-                                    const float f = sc.ks[g] * fac, lr = in ? sc.lv[g] - (float)vexp : 0.f;
-                                    float gm = -INFINITY, w[16], sx = 0.f, sy = 0.f;
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        const bool see = (bits >> (16 * gi + e)) & 1;
-                                        const float y = see ? fmaf(__uint_as_float(x[16 * gi + e]), f, lr - base) : -INFINITY;
-                                        gm = fmaxf(gm, y);
-                                        w[e] = ex2(y);
-                                    }
-                                    top = fmaxf(top, gm - lr);
-#pragma unroll
-                                    for (int e = 0; e < 16; e += 2) add2(sx, sy, w[e], w[e + 1]);
-                                    add = fmaf(sx + sy, ex2(-lr), add);
-                                    if (!in) {
-                                        const float vs = sc.vs[g];
-                                        const int bu = (int)(__float_as_uint(vs) >> 23) & 255;
-                                        const float ratio = bu == 0 ? 0.f : bu > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs * pow2(-vexp);
-#pragma unroll
-                                        for (int e = 0; e < 16; ++e) w[e] = (bits >> (16 * gi + e)) & 1 ? w[e] * ratio : 0.f;      // the ratio may be NaN
-                                    }
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) out[8 * gi + e] = pack2(w[2 * e], w[2 * e + 1]);
-                                }
-                                if (!__any_sync(0xffffffffu, top > kSlack || (m == -INFINITY && top > -INFINITY))) break;
-                                raise(c, top + base);
+                    for (; go && done < 4; done += go ? 2 : 0) {
+                        const float add = weights(std::false_type(), 0u, 0u);
+                        if (__any_sync(0xffffffffu, have && add > kMost)) break;      // the maximum has to move
+                        l += add;
+                        tmem_st32(ts + 16 * done, out);      // over columns of S that have been read
+                    }
+                    go = all;
+#pragma unroll 1
+                    while (go && done < 4) {
+                        const uint32_t b0 = view(done), b1 = view(done + 1);
+                        float add = 0.f;
+                        bool move = __any_sync(0xffffffffu, (b0 | b1) != 0 && m == -INFINITY), moved = false;
+#pragma unroll 1
+                        do {
+                            if (move) {
+                                raise(done, 2, b0 | (unsigned long long)b1 << 32);
+                                moved = true;
+                                go = __all_sync(0xffffffffu, (b0 | b1) == 0 || fabsf(m) < kFar);
+                                if (!go) break;
                             }
-                            l += add;
-                            tmem_st16(ts + 16 * c, out);
-                        }
+                            add = weights(std::true_type(), b0, b1);
+                            move = !moved && __any_sync(0xffffffffu, add > kMost);      // at the true maximum no weight is above 1
+                        } while (move);
+                        if (!go) break;
+                        l += add;
+                        tmem_st32(ts + 16 * done, out);
+                        done += 2;
+                    }
+                    // the same with other scales, or far from zero
+                    const unsigned plain = near ? (unsigned)sc.plain : 0u;
+#pragma unroll 1
+                    for (; done < 4; ++done) {
+                        uint32_t out16[16];
+                        const uint32_t bits = view(done);
+                        float add = 0.f;
+                        bool move = __any_sync(0xffffffffu, bits != 0 && m == -INFINITY), moved = false;
+#pragma unroll 1
+                        do {
+                            if (move) {
+                                raise(done, 1, bits);
+                                moved = true;
+                            }
+                            uint32_t x[32];
+                            tmem_ld32(ts + 32 * done, x);
+                            tmem_ld_wait(x);
+                            const float base = m == -INFINITY ? 0.f : m;
+                            add = 0.f;
+#pragma unroll
+                            for (int gi = 0; gi < 2; ++gi) {
+                                const int g = 2 * done + gi;
+                                const bool in = (plain >> g) & 1;      // the V scale is in the exponent
+                                const float f = sc.ks[g] * fac, lr = in ? sc.lv[g] - (float)vexp : 0.f;
+                                float w[16], sx = 0.f, sy = 0.f;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const bool see = (bits >> (16 * gi + e)) & 1;
+                                    w[e] = ex2(see ? __fmul_rn(__uint_as_float(x[16 * gi + e]), f) - base + lr : -INFINITY);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2) add2(sx, sy, w[e], w[e + 1]);
+                                add = fmaf(sx + sy, ex2(-lr), add);
+                                if (!in) {
+                                    const float vs = sc.vs[g];
+                                    const int bu = (int)(__float_as_uint(vs) >> 23) & 255;
+                                    const float ratio = bu == 0 ? 0.f : bu > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs * pow2(-vexp);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) w[e] = (bits >> (16 * gi + e)) & 1 ? w[e] * ratio : 0.f;      // the ratio may be NaN
+                                }
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) out16[8 * gi + e] = pack2(w[2 * e], w[2 * e + 1]);
+                            }
+                            move = !moved && __any_sync(0xffffffffu, add > kMost);
+                        } while (move);
+                        l += add;
+                        tmem_st16(ts + 16 * done, out16);
                     }
                     tmem_st_wait();
                     tc_fence_before();
@@ -627,22 +697,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 float back = vexp == kMinExp ? 0.f : pow2(vexp);
                 if (whole) back = l != 0.f ? back / l : 0.f;      // no visible token: zeros
-                float *part = parts + (size_t)it.slot * PF + (size_t)r * D;
+                const auto mine = reinterpret_cast<unsigned long long>(whole ? static_cast<void *>(out)
+                                                                             : static_cast<void *>(parts + (size_t)it.slot * PF + (size_t)r * D));
+                auto leave = [&](unsigned at) {                   // bytes at .. at + 2 D - 1 of the rows
+                    __syncwarp();
 #pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        const int src = i * ROWS + sub;
+                        const unsigned long long row = __shfl_sync(0xffffffffu, mine, src) + at;
+                        if (row0 + src < it.rows) *(reinterpret_cast<uint4 *>(row) + ch) = lds128(stage + src * D * 2 + ((ch ^ (src & 7)) << 4));
+                    }
+                    __syncwarp();
+                };
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld32(to + 32 * c, o);
                     tmem_ld_wait(o);
-                    if (!have) continue;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float x[8];
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * back);
+                    if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[e + i]) * back;
-                        if (whole) store8(out + 32 * c + e, x);
-                        else store8(part + 32 * c + e, x);
+                        for (int e = 0; e < 32; e += 8) {
+                            float x[8];
+                            uint4 w;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[e + i]);
+                            store8(reinterpret_cast<T *>(&w), x);
+                            sts128(stage + lane * D * 2 + (((4 * c + e / 8) ^ (lane & 7)) << 4), w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            sts128(stage + lane * D * 2 + (((8 * c % CH + e / 4) ^ (lane & 7)) << 4), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                        if (8 * (c + 1) % CH == 0) leave(32 * c / (D / 2) * D * 2);
                     }
                 }
+                if (whole) leave(0);
                 if (!whole && have) *reinterpret_cast<float2 *>(parts + (size_t)it.slot * PF + (size_t)RT * D + 2 * r) = make_float2(m, l);
                 tc_fence_before();
             }

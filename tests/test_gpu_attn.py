@@ -161,6 +161,42 @@ def test_more_rows_than_tokens(dt, ws):
 
 
 @pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("heads", [(4, 2, 64), (4, 2, 128), (4, 2, 48)])
+@pytest.mark.parametrize("news", [None, [150, 3]])
+def test_scores_far_beyond_the_last_bit_of_the_maximum(dt, heads, news, ws):
+    # scores up to about 1e11, where one step of an f32 is thousands: the output is v of the largest one
+    lens = [400, 37]
+    n_q, n_kv, d = heads
+    c = kvref.Cache(2, lens, n_kv, 32, d, seed=21)
+    got, ref, vmax = run(c, news, dt, n_q, ws, qmul=1e4, scale=1e6)
+    assert np.isfinite(got).all()
+    import torch
+    row_start = None if news is None else np.concatenate([[0], np.cumsum(news)])
+    n_rows = c.n_seq if news is None else int(row_start[-1])
+    w = n_q * d
+    q = torch.from_numpy(np.random.default_rng(1).normal(0, 1e4, (n_rows, w + 16)).astype(np.float32)).to(tdt(dt)).float().numpy()
+    u = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dt]
+    seen = 0
+    for r, (s, pos) in enumerate(kvref.places(c, row_start, n_rows)):
+        t = np.arange(pos + 1)
+        pg = c.table[s, t // c.page]
+        for h in range(n_q):
+            kvh = h // (n_q // n_kv)
+            k = c.k[pg, kvh, t % c.page].astype(np.float64) * c.ks[pg, kvh][:, None]
+            parts = np.abs(k * q[r, h * d:(h + 1) * d].astype(np.float64)).sum(axis=1).max()
+            x = k @ q[r, h * d:(h + 1) * d].astype(np.float64)
+            top = np.sort(x)[-2:]
+            # f32 sums of d products: not decided where the two largest are this close
+            if len(x) > 1 and top[1] - top[0] < 2.0 ** -16 * parts:
+                continue
+            seen += 1
+            at = int(np.argmax(x))
+            v = c.v[pg[at], kvh, at % c.page].astype(np.float64) * c.vs[pg[at], kvh]
+            assert (np.abs(got[r, h] - v) <= (4e-5 + (2.0 ** -11 if dt != "f32" else 0.0)) * np.abs(v).max() + u * np.abs(v)).all()
+    assert seen > 0.9 * n_rows * n_q
+
+
+@pytest.mark.parametrize("dt", DTS)
 @pytest.mark.parametrize("news", [None, [150, 3]])
 def test_one_token_takes_all(dt, news, ws):
     # scores far apart (up to about 1e4): the softmax is one token, and nothing overflows
