@@ -20,7 +20,9 @@ namespace pqk {
 
 constexpr int kAttnMaxGrid = 320;      // CTAs at most (parts in the workspace)
 
-constexpr int kFewTiles = 4;           // a sequence's row tiles that one lane counts by itself
+// A sequence's row tiles that one lane counts by itself; more are spread over the lanes (110 of them, one by one:
+// 14000 cycles before the first unit, spread 8000; up to 4 the plain loop is shorter).
+constexpr int kFewTiles = 4;
 
 // One row tile: its rows, the positions they cover, the token tiles they see.
 struct RowTile {
@@ -56,7 +58,7 @@ struct Cut {
     long long total, size, longer;
     int grid;                         // ranges: CTAs that have work
 
-    // At most `most` ranges, of at least LEAST places (more than an item's cost, so that each has a unit).
+    // At most `most` ranges, of at least LEAST places. A range of an item's cost alone has no unit, and its CTA no work.
     template <int LEAST> static __device__ __forceinline__ Cut make(long long total, const FastDiv &most) {
         Cut c;
         c.total = total;

@@ -10,30 +10,42 @@
 // halves whose products and softmaxes alternate, so that both share one
 // conversion of each K and V tile from 8 bits.  P lies over the S it came from.
 //
-// Bound by the tensor cores (4 x 512 cycles a tile for 256 rows at head size
-// 128) and, close to it, by shared memory (operands of four products, 64 KB of
-// converted codes) and the exponentials (256 x 128 a tile).
+// Each half's chain is softmax -> P V -> S of the next tile, and the two
+// halves' chains share the tensor cores: of a tile's 3400 cycles at head size
+// 128 the products take 2048.  A row's thread needs about 1900 for its 128
+// weights (fma, exponential, sum, packing: 2.5 instructions each, and the
+// reads of tensor memory), the products after it 512 + 512, the hand-overs
+// 400.  2048 rows of 32 heads over 10240 tokens (8 kv heads of 128) take
+// 256 us, 1.2 PFLOP/s of the 1.93 that a large bf16 product reaches; 4 prompts of
+// 1000 to 4096 tokens with a window of 1024 (14 heads of 64 over 2) 88 us, where
+// the items' starts and ends and the masked tiles cost as much as the rest.
+// Measured and not taken: halves of a tile's tokens as products of their own
+// (S: 305 us, P V: 285), with 128 weights held before any is stored 282.
 //
 //   warps 0-7    softmax, thread = row (tensor-memory lane), warps 0-3 the
-//                first half: maximum of S, exponentials, P back to tensor memory; at an item's
-//                start the row of q, at its end the row of the output
-//   warps 8-11   codes -> fp16 into the operand image (rows of 8 x 16 bytes: the
+//                first half: weights of S back to tensor memory; at an item's
+//                start the rows of q, at its end the rows of the output
+//   warps 8-11   codes -> fp16 into operand images (rows of 8 x 16 bytes: the
 //                same image serves as K-major K and as MN-major V)
 //   warp 12      walks the units, TMA of K and V tiles, page numbers and scales
-//   warp 13      one thread issues the products
+//   warp 13      issues the products: the whole warp together, one elected lane
+//                (from a single thread's branch 8 products took 900 cycles to issue, so 400)
 //   warp 14      what the softmax needs of a tile's page scales
-// Shared memory: q 64 KB, converted K and V 32 KB each, three raw tiles 96 KB.
+// Shared memory at head size 128: q 64 KB, a ring of three converted tiles
+// (K and V in turn: with one of each, a conversion waited for the products of the
+// tile before, 341 -> 312 us) 96 KB, four raw ones 64 KB.
 //
 // Per page the weights are formed as exp2(S * f + c), f = q's and K's scales,
 // c = log2(V's scale over a power of two above the largest seen) - maximum:
 // the V scale costs nothing per element; the weight sum undoes it once a page.
 // The running maximum and the power of two lag as in the decode kernel, so O
-// is rescaled (by its own row's thread) only now and then.  A row goes through
-// tensor memory once, 64 columns at a time; columns that pass the maximum by
-// more than its lag are found beside their weights: the thread then moves the
-// maximum (O, the sum and the row's earlier weights of the tile are rescaled)
-// and takes those columns again.  Tiles at an edge of some row's view, or with
-// page scales that are no ordinary positive numbers, take a masking variant.
+// is rescaled (by its own row's thread) only now and then: the maximum when a
+// row's weights of 64 tokens sum to more than 2^15, which keeps each inside
+// fp16 and needs no maximum per element.  P is rounded to fp16 (11 bits, as
+// f16 rows are; bf16 rows have 8), the sum l is taken of the weights before.
+// Tiles at an edge of some row's view take the same step with a mask; tiles
+// with missing pages, with scales that are no ordinary positive numbers, or
+// with maxima past 2^20 (where the V scale would be lost beside it) a slower one.
 
 #include <type_traits>
 
@@ -47,8 +59,11 @@ constexpr int RT = 256, HALF = 128;          // rows of an item, and of each hal
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kWalkWarp = kSoftmaxWarps + kConvertWarps, kMmaWarp = kWalkWarp + 1, kScaleWarp = kWalkWarp + 2;
 constexpr int kThreads = 32 * (kScaleWarp + 1);
-constexpr int kImages = 3, kMeta = 4, kItems = 8, kItemCost = 2;
-constexpr int kLeast = 4;                    // places of a CTA
+constexpr int kImages = 3, kMeta = 4, kItems = 8;
+// An item's rows in and out, its masked tiles and its empty pipeline, in units (2: a prompt of 8192 tokens, 32 heads
+// over 8, 585 us, windowed prompts 94; 6: 470 and 88; 10: 478 and 89).
+constexpr int kItemCost = 6;
+constexpr int kLeast = 4;                    // places of a CTA (8: 64 rows over 4096 tokens 32.6 us, 4: 25.1)
 constexpr int kTcGrid = 160;                 // CTAs at most: one per SM
 constexpr int kTmemCols = 512;
 constexpr float kMost = 32768.f;             // the running maximum moves when a row's weights of one step sum to more: fp16 holds each

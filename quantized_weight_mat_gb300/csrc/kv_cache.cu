@@ -6,7 +6,7 @@
 namespace pqk {
 namespace {
 
-constexpr int kGatherRows = 2;
+constexpr int kGatherRows = 2;      // of a block (8192 rows of 8 heads of 128: one 13.0 us, two 12.0; 7 ragged prompts, 2 of 64: 4.8 and 3.2)
 
 // What the preceding kernels on the stream wrote is complete after this; the
 // next kernel may then be scheduled beside this one.
@@ -172,8 +172,12 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs &p, int b, int
 // that a sequence's rows reach, then the blocks of the query rows.  A block sees every new token of its page and head, so the page's
 // scale needs no other block.  The values are read and rotated once: between the
 // maximum and the codes they wait in registers (SINGLE: one row per sequence,
-// one unit a thread, one warp a block) or as f32 in shared memory.  Bound by memory for prompts,
-// by the chain of dependent loads (length, page, scale) for single tokens.
+// one unit a thread, one warp a block) or as f32 in shared memory.
+// 8192 new tokens of 8 kv heads of 128 with the 32 query heads' rotation take
+// 49.6 us (bf16; 20.6 without q), where the bytes alone need 27: a block's phases
+// (load, maximum, codes) hide each other's latency only across the 6 blocks of an SM.
+// Single tokens are bound by the chain of dependent loads (length, page, scale):
+// 2.5 us for one sequence, 3.8 for 128.
 template <class T, bool SINGLE>
 __global__ void __launch_bounds__(SINGLE ? 32 : 128) kv_append(KvAppendArgs p, int items) {
     constexpr int NT = SINGLE ? 32 : 128;
