@@ -48,6 +48,7 @@ namespace {
 constexpr int kConsumers = 4;                // warps, 32 tokens of a tile each
 constexpr int kThreads = 32 * (kConsumers + 2);
 constexpr int kItemCost = 2;                 // places of an item beside its units (64 ragged sequences: 1: 70.7 us, 2: 65.6, 3: 67.4)
+constexpr int kLeast = 2;                    // places of a CTA (one row over 4096 tokens: 1: 12.7 us, 2: 11.7, 3: 12.7; over 512: 8.6, 9.3, 10.0)
 constexpr int kItems = 8;                    // items that the walking warp may be ahead (more than the tiles it looks up at a time)
 
 template <int D> __host__ __device__ constexpr int tile_bytes() { return KT * D; }
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int g = lane % kGroups, sub = lane / kGroups;
         Walk at;
         long long first, last;
-        const Cut cut = find_range<Walk, kItemCost + 1>(p, at, first, last);
+        const Cut cut = find_range<Walk, kLeast>(p, at, first, last);
         Split split;                       // of the last item: only that can go on in another CTA
         split.c1 = -1;
         if (lane == 0) splits_of(p)[blockIdx.x].c1 = -1;      // should a wait below run out

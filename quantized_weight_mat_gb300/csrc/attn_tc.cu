@@ -63,7 +63,7 @@ constexpr int kImages = 3, kMeta = 4, kItems = 8;
 // An item's rows in and out, its masked tiles and its empty pipeline, in units (2: a prompt of 8192 tokens, 32 heads
 // over 8, 585 us, windowed prompts 94; 6: 470 and 88; 10: 478 and 89).
 constexpr int kItemCost = 6;
-constexpr int kLeast = 4;                    // places of a CTA (8: 64 rows over 4096 tokens 32.6 us, 4: 25.1)
+constexpr int kLeast = 3;                    // places of a CTA (64 rows over 4096 tokens: 8: 32.6 us, 4: 25.0, 3: 24.2, 2: 24.6)
 constexpr int kTcGrid = 160;                 // CTAs at most: one per SM
 constexpr int kTmemCols = 512;
 constexpr float kMost = 32768.f;             // the running maximum moves when a row's weights of one step sum to more: fp16 holds each
@@ -102,6 +102,12 @@ __device__ __forceinline__ void add2(float &sx, float &sy, float x, float y) {
     asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
         : "+f"(sx), "+f"(sy)
         : "f"(x), "f"(y));
+}
+
+// Bits of the f32 with the value of a positive 16-bit pattern (both order as their bits do).
+template <class T> __device__ __forceinline__ uint32_t magnitude(uint32_t bits) {
+    if (std::is_same<T, __nv_bfloat16>::value) return bits << 16;
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)bits)));
 }
 
 // A tile's page scales as the softmax takes them.
@@ -182,6 +188,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&q_ready, kSoftmaxWarps);
         fence_mbar_init();
+    }
+    if (threadIdx.x == 32 * kWalkWarp) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
     }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
@@ -421,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + 128u * half + lanes, to = tmem + 256u + 128u * half + lanes;
         uint32_t unit = 0, tiles = 0;                     // units of the CTA, and those with this half
         bool dead = false;
-        // rows of q come in and rows of the output leave through the 32 rows' part of the q image, 16 bytes a lane,
-        // CH lanes a row, so that global memory sees whole rows
+        // rows of the output leave through the 32 rows' part of the q image, 16 bytes a lane, CH lanes a row, so that
+        // global memory sees whole rows
         constexpr int CH = D / 8, ROWS = 32 / CH;
         const int sub = lane / CH, ch = lane % CH, row0 = HALF * half + 32 * (warp & 3);
         const uint32_t stage = q0 + row0 * D * 2;
@@ -440,38 +450,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (act) {
                 // the row of q: power-of-two scale, fp16, operand image
                 const T *mine = static_cast<const T *>(p.q) + (it.r0 + tok) * p.ldq + (long long)head * D;
-                uint4 w[CH];
+                // 8 rows by 64 bytes a load: whole sectors of global memory, and no two lanes on one bank of the image
+                constexpr int PER = D / 32;
+                uint4 w[4][PER];
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int src = i * ROWS + sub;
-                    const T *row = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), src));
-                    w[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (row0 + src < it.rows) w[i] = *(reinterpret_cast<const uint4 *>(row) + ch);
-                }
-                uint32_t of_mine = 0;
+                for (int i = 0; i < 4; ++i) {
+                    const int src = 8 * i + (lane & 7);
+                    const uint4 *row = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), src));
 #pragma unroll
-                for (int i0 = 0; i0 < CH; i0 += 8) {
-                    uint32_t top[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float x[8];
-                        load8(reinterpret_cast<const T *>(&w[i0 + i]), x);
-                        top[i] = 0;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top[i] = max(top[i], __float_as_uint(x[e]) & 0x7fffffffu);
+                    for (int j = 0; j < PER; ++j) {
+                        w[i][j] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row0 + src < it.rows) w[i][j] = row[4 * j + (lane >> 3)];
                     }
+                }
+                uint32_t top[4];
 #pragma unroll
-                    for (int o = 1; o < CH; o <<= 1)
+                for (int i = 0; i < 4; ++i) {
+                    top[i] = 0;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+                    for (int j = 0; j < PER; ++j)
+                        top[i] = __vmaxu2(top[i], __vmaxu2(__vmaxu2(w[i][j].x & 0x7fff7fffu, w[i][j].y & 0x7fff7fffu),
+                                                           __vmaxu2(w[i][j].z & 0x7fff7fffu, w[i][j].w & 0x7fff7fffu)));
+                    top[i] = magnitude<T>(max(top[i] & 0xffffu, top[i] >> 16));
+                }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t t = __shfl_sync(0xffffffffu, top[i], lane % ROWS * CH);
-                        if (lane / ROWS == i0 + i) of_mine = t;
+                for (int o = 8; o < 32; o <<= 1)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+                uint32_t of_mine = top[0];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (lane >> 3 == i) of_mine = top[i];
+                    const float up = pow2(tc_scale_exponent(top[i]));
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
                         float x[8];
-                        load8(reinterpret_cast<const T *>(&w[i0 + i]), x);
-                        const float up = pow2(tc_scale_exponent(top[i]));
-                        sts128(stage + image_at<D>((i0 + i) * ROWS + sub, ch),
+                        load8(reinterpret_cast<const T *>(&w[i][j]), x);
+                        sts128(stage + image_at<D>(8 * i + (lane & 7), 4 * j + (lane >> 3)),
                                make_uint4(pack2(x[0] * up, x[1] * up), pack2(x[2] * up, x[3] * up), pack2(x[4] * up, x[5] * up),
                                           pack2(x[6] * up, x[7] * up)));
                     }
