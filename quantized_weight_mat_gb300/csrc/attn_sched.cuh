@@ -20,8 +20,8 @@ namespace pqk {
 
 constexpr int kAttnMaxGrid = 320;      // CTAs at most (parts in the workspace)
 
-// A sequence's row tiles that one lane counts by itself; more are spread over the lanes (110 of them, one by one:
-// 14000 cycles before the first unit, spread 8000; up to 4 the plain loop is shorter).
+// A sequence's row tiles that one lane counts by itself; more may be spread over the lanes (4 sequences of 110, one
+// by one: 14000 cycles before the first unit, spread 8000; 32 sequences of 9 the other way round: 20000 spread).
 constexpr int kFewTiles = 4;
 
 // One row tile: its rows, the positions they cover, the token tiles they see.
@@ -160,9 +160,15 @@ template <class Walk> __device__ __forceinline__ long long warp_places(const Att
     walk.m = 0;
     if (walk.s < p.c.n_seq) walk.seq(p);
     const int tiles = walk.m > 0 ? walk.tiles : 0;
-    long long n = tiles > 0 && tiles <= kFewTiles ? walk.places(p) : 0;
-    // sequences of many row tiles one after the other, by all lanes
-    for (unsigned many = __ballot_sync(0xffffffffu, tiles > kFewTiles); many; many &= many - 1) {
+    // a few sequences of many row tiles one after the other, by all lanes: about 4 row tiles' time each, and one more
+    // per 32 of them
+    unsigned many = __ballot_sync(0xffffffffu, tiles > kFewTiles);
+    if (many) {
+        const int most = __reduce_max_sync(0xffffffffu, tiles);
+        if (most <= __popc(many) * (4 + most / 32)) many = 0;
+    }
+    long long n = tiles > 0 && !((many >> lane) & 1) ? walk.places(p) : 0;
+    for (; many; many &= many - 1) {
         const int src = __ffs((int)many) - 1, count = __shfl_sync(0xffffffffu, tiles, src);
         Walk of = walk;
         of.m = __shfl_sync(0xffffffffu, walk.m, src);

@@ -110,6 +110,20 @@ def test_prompts(dt, heads, lens, news, ws):
     check(*run(c, news, dt, n_q, ws), dt)
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("n_seq", [5, 40])
+def test_sequences_of_several_row_tiles(dt, n_seq, ws):
+    # f32: 5 to 8 row tiles each, counted lane by lane or all lanes together
+    rng = np.random.default_rng(n_seq)
+    news = [int(x) for x in rng.integers(17, 31, n_seq)]
+    lens = [m + int(x) for m, x in zip(news, rng.integers(0, 40, n_seq))]
+    news[n_seq // 2], lens[n_seq // 2] = 0, 9
+    news[1], lens[1] = 150, 170
+    c = kvref.Cache(n_seq, lens, 2, 32, 64, seed=31)
+    got, ref, vmax = run(c, news, dt, 8, ws)
+    check(got, ref, vmax, dt)
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16"])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (33, 0), (64, 70), (100, 17), (500, 3), (100000, 5), (2 ** 31 - 1, 2 ** 31 - 1)])
 @pytest.mark.parametrize("news", [None, [3, 1, 40, 150, 0]])
