@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = lane; i < k; i += 32) {
             const float q = (float)(int8_t)__ldg(wr + i);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) acc[b] = fmaf(q, __ldg(x + (int64_t)b * k + i), acc[b]);
+            for (int b = 0; b < NB; ++b) acc[b] = fmaf(q, x[(int64_t)b * k + i], acc[b]);
         }
     }
     const float s = __ldg(reinterpret_cast<const float *>(w + soff) + row);
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(kThreads)
             const float q0 = i4_value(b8 & 15u), q1 = i4_value(b8 >> 4);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                acc[b] = fmaf(q0, __ldg(x + (int64_t)b * k + i), acc[b]);
-                acc[b] = fmaf(q1, __ldg(x + (int64_t)b * k + i + 1), acc[b]);
+                acc[b] = fmaf(q0, x[(int64_t)b * k + i], acc[b]);
+                acc[b] = fmaf(q1, x[(int64_t)b * k + i + 1], acc[b]);
             }
         }
     }

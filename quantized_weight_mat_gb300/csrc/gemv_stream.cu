@@ -1566,7 +1566,7 @@ __device__ __forceinline__ float transposed_sum(float (&v)[V], int lane) {
 // Limb image of NB columns: warp w of block (i, b) converts 256-value block
 // 8i + w of column b (zeros for b >= nb_cols).
 template <int NB>
-__global__ void __launch_bounds__(256) prep_x_nb(const float *__restrict__ x, int k, int nb_cols,
+__global__ void __launch_bounds__(256) prep_x_nb(const float *x, int k, int nb_cols,
                                                  uint8_t *__restrict__ img) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");

@@ -137,7 +137,7 @@ __host__ __device__ constexpr int kmaj_off(int n, int K, int sbo) {
 // super-block's 256 values of the column); see that function.
 
 template <int NBP>
-__global__ void __launch_bounds__(256) prep_x_tc(const float *__restrict__ x, int k, int nb_cols,
+__global__ void __launch_bounds__(256) prep_x_tc(const float *x, int k, int nb_cols,
                                                  uint8_t *__restrict__ img) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256) prep_x_tc(const float *__restrict__ x, in
     const int pos = kpos(K / 8, K % 8);
     float v[NBP];
 #pragma unroll
-    for (int b = 0; b < NBP; ++b) v[b] = b < nb_cols ? __ldg(x + (size_t)b * k + sb * 256 + pos) : 0.f;
+    for (int b = 0; b < NBP; ++b) v[b] = b < nb_cols ? x[(size_t)b * k + sb * 256 + pos] : 0.f;
     // sub-block sums: thread (column, sub-block) for t < NBP * 8, 8 vector loads
     const int sbc = t / 8, sbj = t % 8;
     float4 sv[8];
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(256) prep_x_tc(const float *__restrict__ x, in
     if (t < NBP * 8 && sbc < nb_cols) {
         const float4 *xb = reinterpret_cast<const float4 *>(x + (size_t)sbc * k + sb * 256 + 32 * sbj);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sv[i] = __ldg(xb + i);
+        for (int i = 0; i < 8; ++i) sv[i] = xb[i];
     }
     // max |x| per column: the bit patterns of non-negative floats order like
     // their values (NaN above inf), so an integer reduction gives it
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(256) prep_x_tc(const float *__restrict__ x, in
 // (the mins operand; K slots 8..15 are zero); then the factors 2^-e.  The
 // tile has the size of prep_x_tc's.
 template <int NBP>
-__global__ void __launch_bounds__(256) prep_x_mma(const float *__restrict__ x, int k, int nb_cols,
+__global__ void __launch_bounds__(256) prep_x_mma(const float *x, int k, int nb_cols,
                                                   uint8_t *__restrict__ img) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(256) prep_x_mma(const float *__restrict__ x, i
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     float v[NBP];
 #pragma unroll
-    for (int b = 0; b < NBP; ++b) v[b] = b < nb_cols ? __ldg(x + (size_t)b * k + sb * 256 + t) : 0.f;
+    for (int b = 0; b < NBP; ++b) v[b] = b < nb_cols ? x[(size_t)b * k + sb * 256 + t] : 0.f;
     const int sbc = t / 8, sbj = t % 8;
     float4 sv[8];
 #pragma unroll
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(256) prep_x_mma(const float *__restrict__ x, i
     if (t < NBP * 8 && sbc < nb_cols) {
         const float4 *xb = reinterpret_cast<const float4 *>(x + (size_t)sbc * k + sb * 256 + 32 * sbj);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sv[i] = __ldg(xb + i);
+        for (int i = 0; i < 8; ++i) sv[i] = xb[i];
     }
 #pragma unroll
     for (int b = 0; b < NBP; ++b) {
@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
 // Launched after the main kernel with programmatic dependent launch: it can be
 // resident beside it and waits for the main grid to complete.
 template <int NBP>
-__global__ void __launch_bounds__(TM) tc_finish(const float *__restrict__ partials, float *__restrict__ y,
+__global__ void __launch_bounds__(TM) tc_finish(const float *partials, float *__restrict__ y,
                                                long long ldy, long long total, int nb, int n_out, int nb_cols,
                                                const float *__restrict__ bias) {
     asm volatile("griddepcontrol.launch_dependents;");
@@ -969,8 +969,8 @@ __global__ void __launch_bounds__(TM) tc_finish(const float *__restrict__ partia
 // computed the whole tile, else its CTAs' partial sums added in CTA order
 // (the loads of up to four parts in flight at a time).
 template <int NBP>
-__device__ __forceinline__ void tile_sums(float (&sum)[NBP], int t, int r, const float *__restrict__ partials,
-                                          const float *__restrict__ ytmp, long long total, int nb, int grid) {
+__device__ __forceinline__ void tile_sums(float (&sum)[NBP], int t, int r, const float *partials,
+                                          const float *ytmp, long long total, int nb, int grid) {
     const long long t0 = (long long)t * nb;
     const int cf = item_owner(t0, total, grid), cl = item_owner(t0 + nb - 1, total, grid);
     if (cf == cl) {
@@ -1018,8 +1018,8 @@ __device__ __forceinline__ float silu_tc(float z) { return z / (1.0f + expf(-z))
 // (gate rows) and 2i+1 (up rows).  Launched after the main kernel with
 // programmatic dependent launch, like tc_finish.
 template <int NBP>
-__global__ void __launch_bounds__(2 * TM) tc_finish_swiglu(const float *__restrict__ partials,
-                                                      const float *__restrict__ ytmp, float *__restrict__ h,
+__global__ void __launch_bounds__(2 * TM) tc_finish_swiglu(const float *partials,
+                                                      const float *ytmp, float *__restrict__ h,
                                                       long long ldh, long long total, int nb, int grid, int n_ff,
                                                       int nb_cols) {
     asm volatile("griddepcontrol.launch_dependents;");

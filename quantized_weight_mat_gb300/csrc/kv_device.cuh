@@ -80,18 +80,18 @@ __device__ __forceinline__ void seq_rows(const KvView &c, int s, int &r0, int &n
         n = 1;
         return;
     }
-    const int a = __ldg(c.row_start + s), b = __ldg(c.row_start + s + 1);
+    const int a = c.row_start[s], b = c.row_start[s + 1];
     r0 = min(max(a, 0), c.n_rows);
     n = max(min(b, c.n_rows) - r0, 0);
 }
 
 // Tokens of sequence s that can lie in pages of its table.
-__device__ __forceinline__ int seq_len(const KvView &c, int s) { return max(__ldg(c.len + s), 0); }
+__device__ __forceinline__ int seq_len(const KvView &c, int s) { return max(c.len[s], 0); }
 
 // Page of block j of sequence s, or -1.
 __device__ __forceinline__ int page_of(const KvView &c, int s, int j) {
     if (j < 0 || j >= c.table_ld) return -1;
-    const int p = __ldg(c.table + (long long)s * c.table_ld + j);
+    const int p = c.table[(long long)s * c.table_ld + j];
     return (unsigned)p < (unsigned)c.n_pages ? p : -1;
 }
 

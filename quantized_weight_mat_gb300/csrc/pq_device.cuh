@@ -14,17 +14,19 @@ __device__ __forceinline__ float h2f(uint32_t bits16) {
     return __half2float(__ushort_as_half((unsigned short)(bits16 & 0xffffu)));
 }
 
+// Ordinary loads: a kernel that is scheduled beside its predecessor may read only with them what that one writes.
+// (ld.global.nc is for data that nothing writes while the kernel lives, and need not stay behind griddepcontrol.wait.)
 __device__ __forceinline__ uint32_t ldg_u32(const uint8_t *p) {
-    return __ldg(reinterpret_cast<const unsigned int *>(p));
+    return *reinterpret_cast<const unsigned int *>(p);
 }
 __device__ __forceinline__ uint32_t ldg_u16(const uint8_t *p) {
-    return __ldg(reinterpret_cast<const unsigned short *>(p));
+    return *reinterpret_cast<const unsigned short *>(p);
 }
 __device__ __forceinline__ uint4 ldg_u128(const uint8_t *p) {
-    return __ldg(reinterpret_cast<const uint4 *>(p));
+    return *reinterpret_cast<const uint4 *>(p);
 }
 __device__ __forceinline__ float4 ldg_f4(const float *p) {
-    return __ldg(reinterpret_cast<const float4 *>(p));
+    return *reinterpret_cast<const float4 *>(p);
 }
 
 // Power-of-two scale of x for the fp16 operands of the tensor-core kernels.
