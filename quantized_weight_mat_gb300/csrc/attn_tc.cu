@@ -16,8 +16,8 @@
 // weights (fma, exponential, sum, packing: 2.5 instructions each, and the
 // reads of tensor memory), the products after it 512 + 512, the hand-overs
 // 400.  2048 rows of 32 heads over 10240 tokens (8 kv heads of 128) take
-// 256 us, 1.2 PFLOP/s of the 1.93 that a large bf16 product reaches; 4 prompts of
-// 1000 to 4096 tokens with a window of 1024 (14 heads of 64 over 2) 88 us, where
+// 249 us, 1.2 PFLOP/s of the 1.93 that a large bf16 product reaches; 4 prompts of
+// 1000 to 4096 tokens with a window of 1024 (14 heads of 64 over 2) 86 us, where
 // the items' starts and ends and the masked tiles cost as much as the rest.
 // Measured and not taken: halves of a tile's tokens as products of their own
 // (S: 305 us, P V: 285), with 128 weights held before any is stored 282.
