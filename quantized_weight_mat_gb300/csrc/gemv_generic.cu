@@ -5,8 +5,8 @@
 // description: decoding fused into the mat-vec, no f32 copy of W): the
 // warp walks its row's blocks, each lane decodes 8 weights per Q4_K / Q6_K
 // super-block (or per Q8_0 block group) to f32 in registers, multiplies by
-// x (read through the read-only cache; x is small and shared by every warp
-// of the SM) and accumulates in f32; a shuffle tree reduces the 32 lanes.
+// x (small, shared by every warp of the SM) and accumulates in f32; a shuffle
+// tree reduces the 32 lanes.
 // It serves every case the specialised kernels do not, and is their
 // reference point in the tests.
 
@@ -28,6 +28,10 @@ constexpr int kWarps = kThreads / 32;
 // CUDA graph of back-to-back calls) and compete for the memory system with
 // the launch that runs (Q8_0 896x896 3.65 -> 3.44 us with the order below).
 // Without that launch attribute both instructions do nothing.
+// x, and weights that were not declared static, may be what that kernel writes:
+// the kernels below take them by plain pointers, since a const __restrict__
+// one lets the compiler turn its loads into read-only ones, which need not stay
+// behind the wait.
 __device__ __forceinline__ void dependent_launch_prologue() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -55,7 +59,7 @@ __device__ __forceinline__ void fma8(float (&acc)[NB], const float (&wv)[8], con
 
 template <int NB>
 __global__ void __launch_bounds__(kThreads)
-    gemv_generic_q4_k(const uint8_t *__restrict__ w, int n_out, int k, const float *__restrict__ x,
+    gemv_generic_q4_k(const uint8_t *w, int n_out, int k, const float *x,
                       float *__restrict__ y, int64_t ldy) {
     dependent_launch_prologue();
     const int lane = threadIdx.x & 31;
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int NB>
 __global__ void __launch_bounds__(kThreads)
-    gemv_generic_q6_k(const uint8_t *__restrict__ w, int n_out, int k, const float *__restrict__ x,
+    gemv_generic_q6_k(const uint8_t *w, int n_out, int k, const float *x,
                       float *__restrict__ y, int64_t ldy) {
     dependent_launch_prologue();
     const int lane = threadIdx.x & 31;
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int blk = 0; blk < nb; ++blk) {
         const uint8_t *bp = wr + (int64_t)blk * 210;
         const float d = h2f(ldg_u16(bp + 208));
-        const float ds = d * (float)(int)(int8_t)__ldg(bp + 192 + (lane >> 1));
+        const float ds = d * (float)(int)(int8_t)bp[192 + (lane >> 1)];
         float wv[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int NB>
 __global__ void __launch_bounds__(kThreads)
-    gemv_generic_q8_0(const uint8_t *__restrict__ w, int n_out, int k, const float *__restrict__ x,
+    gemv_generic_q8_0(const uint8_t *w, int n_out, int k, const float *x,
                       float *__restrict__ y, int64_t ldy) {
     dependent_launch_prologue();
     const int lane = threadIdx.x & 31;
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kThreads)
 constexpr int kShortRowBytes = 32 * 34;   // 1088: 32 blocks
 template <int NB>
 __global__ void __launch_bounds__(kThreads)
-    gemv_q8_0_short(const uint8_t *__restrict__ w, int n_out, int k, const float *__restrict__ x,
+    gemv_q8_0_short(const uint8_t *__restrict__ w, int n_out, int k, const float *x,
                     float *__restrict__ y, int64_t ldy) {
     __shared__ __align__(16) uint8_t rows[kWarps][kShortRowBytes + 64];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kThreads)
 // of the row (pq_kfamily.cuh) and multiplies them by x.
 template <int FMT, int NB>
 __global__ void __launch_bounds__(kThreads)
-    gemv_generic_kfamily(const uint8_t *__restrict__ w, int n_out, int k, const float *__restrict__ x,
+    gemv_generic_kfamily(const uint8_t *w, int n_out, int k, const float *x,
                          float *__restrict__ y, int64_t ldy) {
     dependent_launch_prologue();
     constexpr int BB = kBlockBytes[FMT];
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(kThreads)
 // (row starts are then 4-byte aligned), else one code at a time.
 template <int NB>
 __global__ void __launch_bounds__(kThreads)
-    gemv_generic_i8_row(const uint8_t *__restrict__ w, int n_out, int k, const float *__restrict__ x,
+    gemv_generic_i8_row(const uint8_t *w, int n_out, int k, const float *x,
                         float *__restrict__ y, int64_t ldy, int64_t soff) {
     dependent_launch_prologue();
     const int lane = threadIdx.x & 31;
@@ -297,12 +301,12 @@ __global__ void __launch_bounds__(kThreads)
         }
     } else {
         for (int i = lane; i < k; i += 32) {
-            const float q = (float)(int8_t)__ldg(wr + i);
+            const float q = (float)(int8_t)wr[i];
 #pragma unroll
             for (int b = 0; b < NB; ++b) acc[b] = fmaf(q, x[(int64_t)b * k + i], acc[b]);
         }
     }
-    const float s = __ldg(reinterpret_cast<const float *>(w + soff) + row);
+    const float s = reinterpret_cast<const float *>(w + soff)[row];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const float v = warp_sum(acc[b]);
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(kThreads)
 // k % 8 == 0 (row starts are then 4-byte aligned), else 2 codes (one byte).
 template <int NB>
 __global__ void __launch_bounds__(kThreads)
-    gemv_generic_i4_row(const uint8_t *__restrict__ w, int n_out, int k, const float *__restrict__ x,
+    gemv_generic_i4_row(const uint8_t *w, int n_out, int k, const float *x,
                         float *__restrict__ y, int64_t ldy, int64_t soff) {
     dependent_launch_prologue();
     const int lane = threadIdx.x & 31;
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kThreads)
         }
     } else {
         for (int i = 2 * lane; i < k; i += 64) {
-            const uint32_t b8 = __ldg(wr + i / 2);
+            const uint32_t b8 = wr[i / 2];
             const float q0 = i4_value(b8 & 15u), q1 = i4_value(b8 >> 4);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
     }
-    const float s = __ldg(reinterpret_cast<const float *>(w + soff) + row);
+    const float s = reinterpret_cast<const float *>(w + soff)[row];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const float v = warp_sum(acc[b]);

@@ -1264,8 +1264,8 @@ __global__ void __launch_bounds__(threads_for<F::kWarps>(), MINB) gemv_rows(Para
     const int i0v = threadIdx.x;
     if (kVec) {
         if (i0v < nrows) {
-            v0 = F::kRowScaled ? __ldg(p.rscale + r0 + i0v) : __ldg(p.bias + r0 + i0v);
-            if (F::kRowScaled && SW) v1 = __ldg(p.rscale + p.n_ff + r0 + i0v);
+            v0 = F::kRowScaled ? p.rscale[r0 + i0v] : p.bias[r0 + i0v];
+            if (F::kRowScaled && SW) v1 = p.rscale[p.n_ff + r0 + i0v];
         }
     }
     prep_x_all<false, true>(p.x, ximg, xmeta, nb, S, warp, CW, lane);
@@ -1277,14 +1277,14 @@ __global__ void __launch_bounds__(threads_for<F::kWarps>(), MINB) gemv_rows(Para
         }
         for (int i = i0v + CW * 32; i < nrows; i += CW * 32) {
             if constexpr (F::kRowScaled) {
-                rsc[i] = __ldg(p.rscale + r0 + i);
-                if (SW) rsc[p.rows_cap + i] = __ldg(p.rscale + p.n_ff + r0 + i);
+                rsc[i] = p.rscale[r0 + i];
+                if (SW) rsc[p.rows_cap + i] = p.rscale[p.n_ff + r0 + i];
             } else {
-                bsm[i] = __ldg(p.bias + r0 + i);
+                bsm[i] = p.bias[r0 + i];
             }
         }
         if (F::kRowScaled && BIAS)
-            for (int i = i0v; i < nrows; i += CW * 32) bsm[i] = __ldg(p.bias + r0 + i);
+            for (int i = i0v; i < nrows; i += CW * 32) bsm[i] = p.bias[r0 + i];
     }
     named_sync(1, CW * 32);
     if (threadIdx.x == 0) mbar_arrive(&x_bar);   // lifts the producer's in-flight limit

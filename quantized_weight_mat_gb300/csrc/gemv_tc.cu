@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
 template <int NBP>
 __global__ void __launch_bounds__(TM) tc_finish(const float *partials, float *__restrict__ y,
                                                long long ldy, long long total, int nb, int n_out, int nb_cols,
-                                               const float *__restrict__ bias) {
+                                               const float *bias) {
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int grid = (int)gridDim.x, c = (int)blockIdx.x;
