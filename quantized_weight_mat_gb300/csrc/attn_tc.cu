@@ -563,7 +563,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!dead && !mbar_wait(&s_full[half], tiles & 1u)) dead = true;
                     tc_fence_after();
                     // the row's maximum moves to the largest score that it sees (bits) of the n steps from c, if that is
-                    // larger; the weights of the steps before are in place
+                    // larger; the weights of the steps before are in place. It moves to the next whole number: a power of
+                    // two takes the stored fp16 weights along without another rounding, but for those that become smaller
+                    // than 2^-14 of the new largest, which keep an absolute 2^-25 of it (a itself may be far below fp16)
                     auto raise = [&](int c, int n, unsigned long long bits) {
                         float top = -INFINITY;
                         tmem_st_wait();
@@ -579,12 +581,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float a = 1.f;
                         if (top > m) {
-                            a = m == -INFINITY ? 0.f : ex2(m - top);
-                            m = top;
+                            const float up = ceilf(top);
+                            a = m == -INFINITY ? 0.f : pow2((int)fmaxf(m - up, -200.f));
+                            m = up;
                         }
                         l *= a;
                         rescale(a);
-                        const uint32_t a2 = pack2(a, a);
 #pragma unroll 1
                         for (int i = 0; i < c; ++i) {
                             uint32_t w[16];
@@ -592,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_ld_wait(w);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&w[e]), *reinterpret_cast<const __half2 *>(&a2));
-                                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                                w[e] = pack2(f.x * a, f.y * a);
                             }
                             tmem_st16(ts + 16 * i, w);
                         }
