@@ -373,8 +373,11 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
  *         holds before and after a call does not matter.  Calls that may
  *         overlap on the GPU need one each.
  * Accumulation in f32; q (scaled per row by a power of two) and the softmax
- * weights enter the tensor cores as fp16, f32 rows' as fp16 pairs, the codes
- * exactly.  Deterministic.
+ * weights (times their page's V scale over a power of two that follows the row's
+ * largest such product) enter the tensor cores as fp16, f32 rows' as fp16 pairs,
+ * the codes exactly.  So a weight that counts is off by 2^-12 of itself (as a pair
+ * by 2^-22), whatever the pages' scales are beside each other, and what is lost of the
+ * smallest ones stays below 2^-24 of the largest product for each token.  Deterministic.
  */
 int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt,
             const void *q, long long ldq, int n_q, float scale, int window, int n_sink,

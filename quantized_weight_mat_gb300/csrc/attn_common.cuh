@@ -13,7 +13,10 @@ namespace {
 constexpr int KT = 128;                      // tokens per tile
 constexpr int kGroups = KT / 16;             // groups of 16 tokens: always within one page
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMinExp = -200, kMaxExp = 125;   // of V scales: none seen yet, and the largest
+constexpr int kMinExp = -200, kMaxExp = 125;   // of V scales: one that takes no part, and the largest
+constexpr int kLeastExp = -118;              // of a row's reference for V scales: 2^-(kLeastExp - 7) is a normal number, the smallest scale 2^-8 of it
+constexpr int kFarExp = 400;                 // differences of exponents beyond which nothing is left
+constexpr float kNever = 1e30f;              // a maximum that no score passes
 constexpr float kSlack = 8.f;                // the running maximum may lag by this many powers of two
 
 struct TileMeta {

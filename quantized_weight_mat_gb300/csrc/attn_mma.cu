@@ -14,11 +14,14 @@
 // The softmax weights enter in fp16 for bf16 rows (their 11 bits lie far below
 // the output's 8) and as an fp16 pair for f16 and f32 rows (one fp16 would add half
 // as much again to f16's own rounding, and the loads hide the second product), already times
-// their page's V scale over a power of two above the largest one the row has
-// seen: ratios are at most 1 and weights at most the 2^8 that the running
-// maximum may lag behind, so fp16 holds them whatever the scales.  Both
-// references move rarely (the maximum by 2^8, the power of two at 4 to 8 times the
-// scale that set it): rescaling O costs a warp half a tile's time.
+// their page's V scale, over a power of two R that follows the largest product of
+// a weight and its page's scale: not the largest scale, since a page that weighs
+// nothing may have one far above the page that holds the weight.  fp16 holds
+// 2^15 of R down to 2^-24 of it (kLift), so a weight is off by 2^-12 of itself (2^-23 as
+// a pair) or by 2^-32 of the row's largest product.  The sum l is of the weights before,
+// over their own running maximum.  Both references are whole powers of two (no
+// rounding when they move) and move rarely, when a new value passes them by
+// 2^8: rescaling O costs a warp half a tile's time.
 //
 // ldmatrix gives a thread four codes of one token (K) or, transposed in 2-byte
 // units, two elements of two tokens (V): the byte permutes of the conversion
@@ -92,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int RT = 8 * NT, NS = stages<D>(), CH = D / 16;
     constexpr bool PAIR = sizeof(T) == 4;            // q as fp16 pairs
     constexpr bool WPAIR = !std::is_same<T, __nv_bfloat16>::value;      // the weights as fp16 pairs
-    constexpr int kLiftExp = WPAIR ? 7 : 0;          // keeps the low halves of small weights above fp16's last bit
+    constexpr int kLift = 7;                         // weights are at most 2^kSlack R: this far up, fp16 holds them and as many small ones as it can
     constexpr int RLD = red_pitch<D>(), QP = q_pitch<D>();
     constexpr int AHEAD_C = NT == 1 ? CH / 2 : 1;    // K chunk pairs loaded ahead of their use
     using Walk = UnitWalk<RT, KT, kItemCost>;
@@ -277,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t qh[CH][2], ql[PAIR ? CH : 1][2];
     float fac[NT][2];                                // of rows 2t, 2t+1: undoes q's scale, times scale * log2 e
     int pos[NT][2];                                  // their positions, -1 for none
-    float m[NT][2], l[NT][2], o[NT][CH][4];
-    int vexp[NT][2];                                 // V scales are taken over 2^vexp
+    float m[NT][2], l[NT][2], o[NT][CH][4];          // m is a whole number
+    int vexp[NT][2];                                 // O is in units of R = 2^(m + vexp): V scales are taken over 2^vexp
     bool dead = false;
     int slot = 0;
     uint32_t phase = 0;
@@ -309,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int e = 0; e < 2; ++e) {
                     fac[x][e] = q_fac[8 * x + 2 * t + e];
                     pos[x][e] = q_pos[8 * x + 2 * t + e];
-                    m[x][e] = -INFINITY;
+                    m[x][e] = pos[x][e] < 0 ? kNever : -INFINITY;      // a row without tokens has nothing to follow
                     l[x][e] = 0.f;
-                    vexp[x][e] = pos[x][e] < 0 ? kMaxExp : kMinExp;      // a row without tokens takes no page's scale
+                    vexp[x][e] = kLeastExp;
                 }
 #pragma unroll
                 for (int c = 0; c < CH; ++c) o[x][c][0] = o[x][c][1] = o[x][c][2] = o[x][c][3] = 0.f;
@@ -417,37 +420,36 @@ __global__ void __launch_bounds__(kThreads, 2)
                 ve[i] = be == 0 || be > 127 + kMaxExp - 4 ? kMinExp : be - 126;
                 vu[i] = be == 0 ? 0.f : be > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs[i];
 #pragma unroll
-                for (int x = 0; x < NT; ++x) {
+                for (int x = 0; x < NT; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) raise |= s[i][x][e] > m[x][e & 1] + kSlack;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) raise |= ve[i] > vexp[x][e];
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        // the lower of the two references, as a score of this group
+                        const float most = m[x][e] + (kSlack + (float)min(0, vexp[x][e] - ve[i]));
+                        raise |= s[i][x][e] > most || s[i][x][e + 2] > most;
+                    }
             }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(fmaxf(s[0][x][e], s[0][x][e + 2]), fmaxf(s[1][x][e], s[1][x][e + 2]));
-#pragma unroll
-                        for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                        const float mn = fmaxf(m[x][e], top);
-                        float a = m[x][e] == -INFINITY ? 0.f : ex2(m[x][e] - mn);
-                        m[x][e] = mn;
-                        l[x][e] *= a;
-                        // a row takes a page's V scale only if it sees a token of the page
-                        int big = kMinExp;
+                        float top[2];                // of each group
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int b = t0 + 16 * i, ps = pos[x][e];
-                            if (b <= ps && !(p.window > 0 && b >= p.n_sink && b + 15 <= ps - p.window)) big = max(big, ve[i]);
+                            top[i] = fmaxf(s[i][x][e], s[i][x][e + 2]);
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], w));
                         }
-                        if (big > vexp[x][e]) {
-                            big += 2;                // room to grow
-                            a = vexp[x][e] == kMinExp ? 0.f : a * pow2(vexp[x][e] - big);
-                            vexp[x][e] = big;
-                        }
+                        const float mn = fmaxf(m[x][e], ceilf(fmaxf(top[0], top[1])));
+                        const int up = m[x][e] == -INFINITY ? kFarExp : (int)fminf(mn - m[x][e], (float)kFarExp);
+                        // R stays while m moves, as far as vexp can follow, unless the group's products are above it
+                        int vn = max(vexp[x][e] - up, kLeastExp);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) vn = max(vn, (int)ceilf(fmaxf(top[i] - mn, -(float)kFarExp)) + ve[i]);
+                        const float a = pow2(vexp[x][e] - up - vn);
+                        l[x][e] *= pow2(-up);
+                        m[x][e] = mn;
+                        vexp[x][e] = vn;
 #pragma unroll
                         for (int c = 0; c < CH; ++c) {
                             o[x][c][e] *= a;
@@ -455,11 +457,19 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
             }
-            float vinv[NT][2];
+            float vrel[2][NT][2];                    // the V scales over R / 2^m
 #pragma unroll
             for (int x = 0; x < NT; ++x)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) vinv[x][e] = pow2(kLiftExp - vexp[x][e]);
+                for (int e = 0; e < 2; ++e) {
+                    const float inv = pow2(kLift - vexp[x][e]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        vrel[i][x][e] = vu[i] * inv;
+                        // a scale that far above R belongs to weights near 2^-126: they must not become 0 times infinity
+                        if (fabsf(vrel[i][x][e]) == INFINITY) vrel[i][x][e] = copysignf(pow2(126), vu[i]);
+                    }
+                }
             uint32_t ph[2][NT][2], pl[2][WPAIR ? NT : 1][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -471,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         for (int e = 0; e < 4; ++e) {
                             w[e] = ex2(s[i][x][e] - m[x][e & 1]);
                             l[x][e & 1] += w[e];
-                            w[e] *= vu[i] * vinv[x][e & 1];
+                            w[e] *= vrel[i][x][e & 1];
                         }
                     } else {
                         // zeros before the sum (a row without tokens has inf - inf here) and after the scale (a
@@ -481,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             const bool see = !(hidden & (1u << (4 * (2 * x + i) + e)));
                             w[e] = see ? ex2(s[i][x][e] - m[x][e & 1]) : 0.f;
                             l[x][e & 1] += w[e];
-                            w[e] = see ? w[e] * (vu[i] * vinv[x][e & 1]) : 0.f;
+                            w[e] = see ? w[e] * vrel[i][x][e & 1] : 0.f;
                         }
                     }
 #pragma unroll
@@ -562,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if ((t >> 1) == hf) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float back = vexp[x][e] == kMinExp ? 0.f : pow2(vexp[x][e] - kLiftExp);
+                            const float back = pow2(vexp[x][e] - kLift);
                             float *mine = red + (warp * 4 + 2 * (t & 1) + e) * RLD + 2 * g;
 #pragma unroll
                             for (int c = 0; c < CH; ++c)

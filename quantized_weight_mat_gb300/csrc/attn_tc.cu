@@ -36,13 +36,14 @@
 // tile before, 341 -> 312 us) 96 KB, four raw ones 64 KB.
 //
 // Per page the weights are formed as exp2(S * f + c), f = q's and K's scales,
-// c = log2(V's scale over a power of two above the largest seen) - maximum:
-// the V scale costs nothing per element; the weight sum undoes it once a page.
-// The running maximum and the power of two lag as in the decode kernel, so O
-// is rescaled (by its own row's thread) only now and then: the maximum when a
-// row's weights of 64 tokens sum to more than 2^15, which keeps each inside
+// c = log2(V's scale) - log2 R, R a power of two that follows the largest product of
+// a weight and its page's V scale, as in the decode kernel: the V scale costs
+// nothing per element; the weight sum undoes it once a page.
+// The running maximum and R lag as in the decode kernel, so O
+// is rescaled (by its own row's thread) only now and then: when a
+// row's weights of 64 tokens, with or without the scales, sum to more than 2^15, which keeps each inside
 // fp16 and needs no maximum per element.  P is rounded to fp16 (11 bits, as
-// f16 rows are; bf16 rows have 8), the sum l is taken of the weights before.
+// f16 rows are; bf16 rows have 8; below 2^-14 of R an absolute 2^-25 of it), the sum l is taken of the weights before.
 // Tiles at an edge of some row's view take the same step with a mask; tiles
 // with missing pages, with scales that are no ordinary positive numbers, or
 // with maxima past 2^20 (where the V scale would be lost beside it) a slower one.
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&q_ready);
 
             float m = -INFINITY, l = 0.f;
-            int vexp = kMinExp;
+            int vexp = kLeastExp;                         // O is in units of 2^(m + vexp), m a whole number
             const int n = it.n;
             for (int i = 0; i < n; ++i, ++unit) {
                 const TileScales &sc = scales[unit % kMeta];
@@ -533,41 +534,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_st_wait();
                     };
-                    // ---- the V scales' reference; mostly all rows see the whole tile and nothing moves
+                    // ---- mostly all rows see the whole tile. V scales in the exponent: at most 2^60 below the reference, which
+                    // may move to ve_max, and beside a maximum whose last bit does not swallow them
                     bool near = true, all = true;
-                    const bool quick = __all_sync(0xffffffffu, sc.quick && (!have || (whole_view() && fabsf(m) < kFar && sc.ve_max <= vexp && sc.lv_min - (float)vexp > -60.f)));
+                    const bool quick = __all_sync(0xffffffffu, sc.quick && (!have || (whole_view() && fabsf(m) < kFar && sc.lv_min - (float)vexp > -60.f)));
                     if (__builtin_expect(!quick, 0)) {
-                        // V scales in the exponent: at most 2^60 below the reference, which may move to ve_max + 2, and beside
-                        // a maximum whose last bit does not swallow them
-                        near = p.scale >= 0.f && __all_sync(0xffffffffu, !have || ((fabsf(m) < kFar || m == -INFINITY) && sc.lv_min - (float)max(vexp, sc.ve_max + 2) > -60.f));
+                        near = p.scale >= 0.f && __all_sync(0xffffffffu, !have || (m == -INFINITY ? sc.lv_min - (float)(sc.ve_max + 2) > -60.f
+                                                                                                   : fabsf(m) < kFar && sc.lv_min - (float)max(vexp, sc.ve_max + 2) > -60.f));
                         all = near && sc.plain == (1 << kGroups) - 1;
-                        int big = kMinExp;
-                        if (__any_sync(0xffffffffu, sc.ve_max > vexp)) {
-#pragma unroll 1
-                            for (int c = 0; c < KT / 32; ++c) {
-                                const uint32_t bits = view(c);
-                                if (bits & 0xffffu) big = max(big, sc.ve[2 * c]);
-                                if (bits >> 16) big = max(big, sc.ve[2 * c + 1]);
-                            }
-                        }
-                        if (__any_sync(0xffffffffu, big > vexp)) {
-                            float a = 1.f;
-                            if (big > vexp) {
-                                big += 2;                 // room to grow
-                                a = vexp == kMinExp ? 0.f : pow2(vexp - big);
-                                vexp = big;
-                            }
-                            rescale(a);
-                        }
                     }
                     if (!dead && !mbar_wait(&s_full[half], tiles & 1u)) dead = true;
                     tc_fence_after();
-                    // the row's maximum moves to the largest score that it sees (bits) of the n steps from c, if that is
-                    // larger; the weights of the steps before are in place. It moves to the next whole number: a power of
-                    // two takes the stored fp16 weights along without another rounding, but for those that become smaller
-                    // than 2^-14 of the new largest, which keep an absolute 2^-25 of it (a itself may be far below fp16)
+                    // The row's references move, if they are smaller, to the largest score that it sees (bits) of the n steps
+                    // from c, and to the largest one times its page's V scale; the weights of the steps before are in place.
+                    // Both are whole numbers: a power of two takes the stored fp16 weights along without another rounding, but
+                    // for those that become smaller than 2^-14 of the new largest, which keep an absolute 2^-25 of it.
                     auto raise = [&](int c, int n, unsigned long long bits) {
-                        float top = -INFINITY;
+                        float top = -INFINITY, tv = -INFINITY;      // tv: the largest score plus V exponent, less top
                         tmem_st_wait();
 #pragma unroll 1
                         for (int g = 2 * c; g < 2 * (c + n); ++g, bits >>= 16) {
@@ -575,17 +558,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_ld16(ts + 16 * g, x);
                             tmem_ld_wait(x);
                             const float f = sc.ks[g] * fac;
+                            float most = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                if ((bits >> e) & 1) top = fmaxf(top, __fmul_rn(__uint_as_float(x[e]), f));
+                                if ((bits >> e) & 1) most = fmaxf(most, __fmul_rn(__uint_as_float(x[e]), f));
+                            if (most > -INFINITY) {
+                                const float t = fmaxf(top, most);
+                                tv = fmaxf(tv + (top - t), (float)sc.ve[g] + (most - t));
+                                top = t;
+                            }
                         }
                         float a = 1.f;
-                        if (top > m) {
-                            const float up = ceilf(top);
-                            a = m == -INFINITY ? 0.f : pow2((int)fmaxf(m - up, -200.f));
-                            m = up;
+                        if (top > -INFINITY) {
+                            const float mn = fmaxf(m, ceilf(top));
+                            const int up = m == -INFINITY ? kFarExp : (int)fminf(mn - m, (float)kFarExp);
+                            // O's unit 2^(m + vexp) stays while m moves, as far as vexp can follow
+                            const int vn = max(max(vexp - up, kLeastExp), (int)ceilf(fmaxf(tv + (top - mn), -(float)kFarExp)));
+                            a = pow2(vexp - up - vn);
+                            l *= pow2(-up);
+                            m = mn;
+                            vexp = vn;
                         }
-                        l *= a;
                         rescale(a);
 #pragma unroll 1
                         for (int i = 0; i < c; ++i) {
@@ -601,12 +594,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     };
                     int done = 0;                             // steps of 32 columns
-                    // weights of the 64 tokens from step done, of those in b0 and b1 if MASK: fp16 pairs, and their sum
+                    // weights of the 64 tokens from step done, of those in b0 and b1 if MASK: fp16 pairs times their V scales, the
+                    // sum without the scales, and with them (sw)
                     uint32_t out[32];
+                    float sw;
                     auto weights = [&](auto mask, uint32_t b0, uint32_t b1) {
                         constexpr bool MASK = decltype(mask)::value;
                         uint32_t x[2][16];
                         float add = 0.f;
+                        sw = 0.f;
                         tmem_ld16(ts + 32 * done, x[0]);
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
@@ -627,7 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 add2(sx, sy, wx, wy);
                                 out[8 * g + e / 2] = pack2(wx, wy);
                             }
-                            add = fmaf(sx + sy, undo, add);
+                            sx += sy;
+                            sw += sx;
+                            add = fmaf(sx, undo, add);
                         }
                         return add;
                     };
@@ -635,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (; go && done < 4; done += go ? 2 : 0) {
                         const float add = weights(std::false_type(), 0u, 0u);
-                        if (__any_sync(0xffffffffu, have && add > kMost)) break;      // the maximum has to move
+                        if (__any_sync(0xffffffffu, have && fmaxf(add, sw) > kMost)) break;      // a reference has to move
                         l += add;
                         tmem_st32(ts + 16 * done, out);      // over columns of S that have been read
                     }
@@ -654,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!go) break;
                             }
                             add = weights(std::true_type(), b0, b1);
-                            move = !moved && __any_sync(0xffffffffu, add > kMost);      // at the true maximum no weight is above 1
+                            move = !moved && __any_sync(0xffffffffu, fmaxf(add, sw) > kMost);      // at the true maximum no weight is above 1
                         } while (move);
                         if (!go) break;
                         l += add;
@@ -679,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_ld32(ts + 32 * done, x);
                             tmem_ld_wait(x);
                             const float base = m == -INFINITY ? 0.f : m;
-                            add = 0.f;
+                            add = sw = 0.f;
 #pragma unroll
                             for (int gi = 0; gi < 2; ++gi) {
                                 const int g = 2 * done + gi;
@@ -697,14 +695,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!in) {
                                     const float vs = sc.vs[g];
                                     const int bu = (int)(__float_as_uint(vs) >> 23) & 255;
-                                    const float ratio = bu == 0 ? 0.f : bu > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs * pow2(-vexp);
+                                    float ratio = bu == 0 ? 0.f : bu > 127 + kMaxExp - 4 ? __int_as_float(0x7fc00000) : vs * pow2(-vexp);
+                                    // a scale that far above belongs to weights near 2^-126: not 0 times infinity
+                                    if (fabsf(ratio) == INFINITY) ratio = copysignf(pow2(126), vs);
+                                    sx = sy = 0.f;
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) w[e] = (bits >> (16 * gi + e)) & 1 ? w[e] * ratio : 0.f;      // the ratio may be NaN
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) add2(sx, sy, fabsf(w[e]), fabsf(w[e + 1]));
                                 }
+                                sw += sx + sy;
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) out16[8 * gi + e] = pack2(w[2 * e], w[2 * e + 1]);
                             }
-                            move = !moved && __any_sync(0xffffffffu, add > kMost);
+                            move = !moved && __any_sync(0xffffffffu, fmaxf(add, sw) > kMost);
                         } while (move);
                         l += add;
                         tmem_st16(ts + 16 * done, out16);
@@ -727,7 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (act) {
                 if (!dead && !mbar_wait(&pv_done[half], (tiles + 1) & 1u)) dead = true;
                 tc_fence_after();
-                float back = vexp == kMinExp ? 0.f : pow2(vexp);
+                // in two factors where 2^vexp over the sum would not be a normal number
+                const bool tiny = __any_sync(0xffffffffu, vexp < -60);
+                const float rest = vexp < -60 ? pow2(-60) : 1.f;
+                float back = pow2(vexp < -60 ? vexp + 60 : vexp);
                 if (whole) back = l != 0.f ? back / l : 0.f;      // no visible token: zeros
                 const auto mine = reinterpret_cast<unsigned long long>(whole ? static_cast<void *>(out)
                                                                              : static_cast<void *>(parts + (size_t)it.slot * PF + (size_t)r * D));
@@ -748,6 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * back);
+                    if (tiny) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * rest);
+                    }
                     if (whole) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
