@@ -324,7 +324,8 @@ typedef struct pq_kv_cache {
  *   k, v       device [n_rows][n_kv * d] of type dt, row strides ldk, ldv in
  *              elements (columns of a fused QKV output pass as they are)
  *   q, q_out   NULL, or device [n_rows][n_q * d] with row strides ldq, ldqo:
- *              q is rotated too and stored to q_out; q_out may be q itself
+ *              q is rotated too and stored to q_out; q_out may be q itself, and
+ *              overlaps neither k nor v (other columns of their rows are no overlap)
  *   rope_cos, rope_sin  device f32 [n_pos][rot/2], 16-byte aligned: row p is
  *              the angle's cosine and sine at position p, for each pair.  The
  *              first rot elements of every head are rotated (rot a multiple of

@@ -58,6 +58,28 @@ int64_t rows_bytes(int64_t ld, int64_t width, int n_rows, int eb) {
     return n_rows > 0 ? ((int64_t)(n_rows - 1) * ld + width) * eb : 0;
 }
 
+// n_rows rows of `width` elements of `eb` bytes, `ld` apart (checked by check_rows).
+struct Rows {
+    const void *p;
+    int64_t ld, width;
+    int n_rows, eb;
+    int64_t bytes() const { return rows_bytes(ld, width, n_rows, eb); }
+};
+
+// Whether two sets of rows share a byte: with one stride by the columns (row i of a against row i + k of b),
+// else by the whole spans, gaps between the rows included.
+bool rows_overlap(const Rows &a, const Rows &b) {
+    if (a.n_rows == 0 || b.n_rows == 0) return false;
+    if (a.ld * a.eb != b.ld * b.eb) return span_overlaps(a.p, a.bytes(), b.p, b.bytes());
+    const int64_t ld = a.ld * a.eb, wa = a.width * a.eb, wb = b.width * b.eb;
+    const int64_t delta = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+    // the first k with b's row ending behind the start of a's: delta + k * ld > -wb
+    const int64_t from = -wb - delta;
+    int64_t k = (from >= 0 ? from / ld : -((-from + ld - 1) / ld)) + 1;
+    if (k < 1 - a.n_rows) k = 1 - a.n_rows;
+    return k < b.n_rows && delta + k * ld < wa && delta + k * ld > -wb;
+}
+
 bool touches_cache(const void *p, int64_t bytes, const pq_kv_cache &c) {
     const int64_t cb = cache_bytes(c), sb = 4 * (int64_t)c.n_pages * c.n_kv;
     return span_overlaps(p, bytes, c.k, cb) || span_overlaps(p, bytes, c.v, cb) ||
@@ -117,10 +139,12 @@ int pq_kv_append(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
         if ((st = check_rows(q, ldq, qw, n_rows, eb)) || (st = check_rows(q_out, ldqo, qw, n_rows, eb))) return st;
         const int64_t ob = rows_bytes(ldqo, qw, n_rows, eb);
         const bool in_place = q_out == q && ldqo == ldq;
-        // in place, k and v may be other columns of the same rows
-        if (!in_place && (span_overlaps(q_out, ob, q, rows_bytes(ldq, qw, n_rows, eb)) ||
-                          span_overlaps(q_out, ob, k, rows_bytes(ldk, kw, n_rows, eb)) ||
-                          span_overlaps(q_out, ob, v, rows_bytes(ldv, kw, n_rows, eb))))
+        const Rows to{q_out, ldqo, qw, n_rows, eb};
+        // k and v are read while q is written; in place they may be other columns of the same rows
+        if (in_place ? rows_overlap(to, {k, ldk, kw, n_rows, eb}) || rows_overlap(to, {v, ldv, kw, n_rows, eb})
+                     : span_overlaps(q_out, ob, q, rows_bytes(ldq, qw, n_rows, eb)) ||
+                           span_overlaps(q_out, ob, k, rows_bytes(ldk, kw, n_rows, eb)) ||
+                           span_overlaps(q_out, ob, v, rows_bytes(ldv, kw, n_rows, eb)))
             return PQ_ERR_ARG;
         if (touches_cache(q_out, ob, c)) return PQ_ERR_ARG;
     }
