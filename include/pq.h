@@ -325,7 +325,8 @@ typedef struct pq_kv_cache {
  *              elements (columns of a fused QKV output pass as they are)
  *   q, q_out   NULL, or device [n_rows][n_q * d] with row strides ldq, ldqo:
  *              q is rotated too and stored to q_out; q_out may be q itself, and
- *              overlaps neither k nor v (other columns of their rows are no overlap)
+ *              overlaps neither k nor v nor another part of q (other columns of
+ *              their rows, at one stride, are no overlap)
  *   rope_cos, rope_sin  device f32 [n_pos][rot/2], 16-byte aligned: row p is
  *              the angle's cosine and sine at position p, for each pair.  The
  *              first rot elements of every head are rotated (rot a multiple of
@@ -369,7 +370,8 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
  *
  *   q     device [n_rows][n_q * d] of type dt, row stride ldq (elements)
  *   out   device [n_rows][n_q * d] of type dt, row stride ldo; overlaps
- *         neither q nor the cache
+ *         neither q (other columns of its rows, at one stride, are no overlap)
+ *         nor the cache
  *   ws    device, 16-byte aligned, at least pq_attn_ws_bytes(...) bytes; what it
  *         holds before and after a call does not matter.  Calls that may
  *         overlap on the GPU need one each.

@@ -140,11 +140,9 @@ int pq_kv_append(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
         const int64_t ob = rows_bytes(ldqo, qw, n_rows, eb);
         const bool in_place = q_out == q && ldqo == ldq;
         const Rows to{q_out, ldqo, qw, n_rows, eb};
-        // k and v are read while q is written; in place they may be other columns of the same rows
-        if (in_place ? rows_overlap(to, {k, ldk, kw, n_rows, eb}) || rows_overlap(to, {v, ldv, kw, n_rows, eb})
-                     : span_overlaps(q_out, ob, q, rows_bytes(ldq, qw, n_rows, eb)) ||
-                           span_overlaps(q_out, ob, k, rows_bytes(ldk, kw, n_rows, eb)) ||
-                           span_overlaps(q_out, ob, v, rows_bytes(ldv, kw, n_rows, eb)))
+        // q, k and v are read while q_out is written
+        if ((!in_place && rows_overlap(to, {q, ldq, qw, n_rows, eb})) || rows_overlap(to, {k, ldk, kw, n_rows, eb}) ||
+            rows_overlap(to, {v, ldv, kw, n_rows, eb}))
             return PQ_ERR_ARG;
         if (touches_cache(q_out, ob, c)) return PQ_ERR_ARG;
     }
@@ -212,7 +210,7 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     if ((uintptr_t)ws % 16) return PQ_ERR_ALIGN;
     if (ws_bytes < pq_attn_ws_bytes(n_q, c.n_kv, c.d)) return PQ_ERR_WS;
     const int64_t ob = rows_bytes(ldo, w, n_rows, eb), qb = rows_bytes(ldq, w, n_rows, eb);
-    if (span_overlaps(out, ob, q, qb) || touches_cache(out, ob, c) || span_overlaps(ws, (int64_t)ws_bytes, out, ob) ||
+    if (rows_overlap({out, ldo, w, n_rows, eb}, {q, ldq, w, n_rows, eb}) || touches_cache(out, ob, c) || span_overlaps(ws, (int64_t)ws_bytes, out, ob) ||
         span_overlaps(ws, (int64_t)ws_bytes, q, qb) || touches_cache(ws, (int64_t)ws_bytes, c))
         return PQ_ERR_ARG;
     const DeviceInfo *dev = nullptr;
