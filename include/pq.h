@@ -304,6 +304,10 @@ int pq_gemv_noalloc(pq_fmt fmt, const void *w_blocks, int n_out, int k,
  * written, not visible, and reads as zeros.  So an idle slot of a batch has
  * len 0.  Table, len and row_start are read on the device: entries out of
  * range are never followed.
+ *
+ * What a call writes overlaps nothing else that it writes or reads (PQ_ERR_ARG),
+ * but for q_out being q.  Sets of rows are compared by their columns where their
+ * strides are equal, else by all bytes from the first row to the last.
  */
 typedef enum { PQ_F32 = 0, PQ_F16 = 1, PQ_BF16 = 2 } pq_dtype;
 
@@ -324,9 +328,7 @@ typedef struct pq_kv_cache {
  *   k, v       device [n_rows][n_kv * d] of type dt, row strides ldk, ldv in
  *              elements (columns of a fused QKV output pass as they are)
  *   q, q_out   NULL, or device [n_rows][n_q * d] with row strides ldq, ldqo:
- *              q is rotated too and stored to q_out; q_out may be q itself, and
- *              overlaps neither k nor v nor another part of q (other columns of
- *              their rows, at one stride, are no overlap)
+ *              q is rotated too and stored to q_out; q_out may be q itself
  *   rope_cos, rope_sin  device f32 [n_pos][rot/2], 16-byte aligned: row p is
  *              the angle's cosine and sine at position p, for each pair.  The
  *              first rot elements of every head are rotated (rot a multiple of
@@ -369,9 +371,7 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
  * gives zeros.  The tokens of this call must have been appended before it.
  *
  *   q     device [n_rows][n_q * d] of type dt, row stride ldq (elements)
- *   out   device [n_rows][n_q * d] of type dt, row stride ldo; overlaps
- *         neither q (other columns of its rows, at one stride, are no overlap)
- *         nor the cache
+ *   out   device [n_rows][n_q * d] of type dt, row stride ldo
  *   ws    device, 16-byte aligned, at least pq_attn_ws_bytes(...) bytes; what it
  *         holds before and after a call does not matter.  Calls that may
  *         overlap on the GPU need one each.

@@ -80,12 +80,36 @@ bool rows_overlap(const Rows &a, const Rows &b) {
     return k < b.n_rows && delta + k * ld < wa && delta + k * ld > -wb;
 }
 
-bool touches_cache(const void *p, int64_t bytes, const pq_kv_cache &c) {
-    const int64_t cb = cache_bytes(c), sb = 4 * (int64_t)c.n_pages * c.n_kv;
+int64_t scale_bytes(const pq_kv_cache &c) { return 4 * (int64_t)c.n_pages * c.n_kv; }
+
+// What every entry reads of the places: table, lengths, row_start.
+bool touches_places(const void *p, int64_t bytes, const pq_kv_cache &c, const int *row_start) {
+    return span_overlaps(p, bytes, c.table, 4 * (int64_t)c.n_seq * c.table_ld) ||
+           span_overlaps(p, bytes, c.len, 4 * (int64_t)c.n_seq) ||
+           (row_start && span_overlaps(p, bytes, row_start, 4 * ((int64_t)c.n_seq + 1)));
+}
+
+// Codes and scales, which an append writes.
+bool touches_values(const void *p, int64_t bytes, const pq_kv_cache &c) {
+    const int64_t cb = cache_bytes(c), sb = scale_bytes(c);
     return span_overlaps(p, bytes, c.k, cb) || span_overlaps(p, bytes, c.v, cb) ||
-           span_overlaps(p, bytes, c.k_scale, sb) || span_overlaps(p, bytes, c.v_scale, sb) ||
-           span_overlaps(p, bytes, c.table, 4 * (int64_t)c.n_seq * c.table_ld) ||
-           span_overlaps(p, bytes, c.len, 4 * (int64_t)c.n_seq);
+           span_overlaps(p, bytes, c.k_scale, sb) || span_overlaps(p, bytes, c.v_scale, sb);
+}
+
+bool touches_cache(const void *p, int64_t bytes, const pq_kv_cache &c, const int *row_start) {
+    return touches_values(p, bytes, c) || touches_places(p, bytes, c, row_start);
+}
+
+// Whether the buffers that an append writes overlap each other, or the places that it reads.
+bool cache_overlaps_itself(const pq_kv_cache &c, const int *row_start) {
+    const void *p[4] = {c.k, c.v, c.k_scale, c.v_scale};
+    const int64_t n[4] = {cache_bytes(c), cache_bytes(c), scale_bytes(c), scale_bytes(c)};
+    for (int i = 0; i < 4; ++i) {
+        if (touches_places(p[i], n[i], c, row_start)) return true;
+        for (int j = 0; j < i; ++j)
+            if (span_overlaps(p[i], n[i], p[j], n[j])) return true;
+    }
+    return false;
 }
 
 KvView view_of(const pq_kv_cache &c, const int *row_start, int n_rows) {
@@ -128,8 +152,11 @@ int pq_kv_append(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
         if (!rope_cos || !rope_sin || n_pos <= 0) return PQ_ERR_ARG;
         if ((uintptr_t)rope_cos % 16 || (uintptr_t)rope_sin % 16) return PQ_ERR_ALIGN;
     }
-    if (touches_cache(k, rows_bytes(ldk, kw, n_rows, eb), c) || touches_cache(v, rows_bytes(ldv, kw, n_rows, eb), c))
+    if (cache_overlaps_itself(c, row_start) || touches_values(k, rows_bytes(ldk, kw, n_rows, eb), c) ||
+        touches_values(v, rows_bytes(ldv, kw, n_rows, eb), c))
         return PQ_ERR_ARG;
+    const int64_t rope_bytes = 4 * (int64_t)n_pos * (rot / 2);
+    if (rot > 0 && (touches_values(rope_cos, rope_bytes, c) || touches_values(rope_sin, rope_bytes, c))) return PQ_ERR_ARG;
     if (!q != !q_out) return PQ_ERR_ARG;
     if (q) {
         if (n_q <= 0) return PQ_ERR_ARG;
@@ -144,7 +171,9 @@ int pq_kv_append(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
         if ((!in_place && rows_overlap(to, {q, ldq, qw, n_rows, eb})) || rows_overlap(to, {k, ldk, kw, n_rows, eb}) ||
             rows_overlap(to, {v, ldv, kw, n_rows, eb}))
             return PQ_ERR_ARG;
-        if (touches_cache(q_out, ob, c)) return PQ_ERR_ARG;
+        if (touches_cache(q_out, ob, c, row_start) || touches_values(q, rows_bytes(ldq, qw, n_rows, eb), c)) return PQ_ERR_ARG;
+        if (rot > 0 && (span_overlaps(q_out, ob, rope_cos, rope_bytes) || span_overlaps(q_out, ob, rope_sin, rope_bytes)))
+            return PQ_ERR_ARG;
     }
     if ((st = check_gb300())) return st;
     if (n_rows == 0) return PQ_OK;
@@ -178,7 +207,8 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
     const pq_kv_cache &c = *cache;
     const int64_t w = (int64_t)c.n_kv * c.d;
     if ((st = check_rows(k_out, ldk, w, n_rows, eb)) || (st = check_rows(v_out, ldv, w, n_rows, eb))) return st;
-    if (touches_cache(k_out, rows_bytes(ldk, w, n_rows, eb), c) || touches_cache(v_out, rows_bytes(ldv, w, n_rows, eb), c))
+    if (touches_cache(k_out, rows_bytes(ldk, w, n_rows, eb), c, row_start) ||
+        touches_cache(v_out, rows_bytes(ldv, w, n_rows, eb), c, row_start))
         return PQ_ERR_ARG;
     if ((st = check_gb300())) return st;
     if (n_rows == 0) return PQ_OK;
@@ -210,8 +240,8 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     if ((uintptr_t)ws % 16) return PQ_ERR_ALIGN;
     if (ws_bytes < pq_attn_ws_bytes(n_q, c.n_kv, c.d)) return PQ_ERR_WS;
     const int64_t ob = rows_bytes(ldo, w, n_rows, eb), qb = rows_bytes(ldq, w, n_rows, eb);
-    if (rows_overlap({out, ldo, w, n_rows, eb}, {q, ldq, w, n_rows, eb}) || touches_cache(out, ob, c) || span_overlaps(ws, (int64_t)ws_bytes, out, ob) ||
-        span_overlaps(ws, (int64_t)ws_bytes, q, qb) || touches_cache(ws, (int64_t)ws_bytes, c))
+    if (rows_overlap({out, ldo, w, n_rows, eb}, {q, ldq, w, n_rows, eb}) || touches_cache(out, ob, c, row_start) || span_overlaps(ws, (int64_t)ws_bytes, out, ob) ||
+        span_overlaps(ws, (int64_t)ws_bytes, q, qb) || touches_cache(ws, (int64_t)ws_bytes, c, row_start))
         return PQ_ERR_ARG;
     const DeviceInfo *dev = nullptr;
     if ((st = check_gb300(&dev))) return st;

@@ -4,7 +4,8 @@ dereferenced: every call here is refused, or stops at the device check)."""
 import pytest
 
 import quantized_weight_mat_gb300 as pq
-from test_kv_refusals import KO, OUT, QKV, VO, WIDTH, append, attn, built, cache  # noqa: F401
+from test_kv_refusals import (COS, K, KO, KS, LEN, OUT, QKV, ROWS, SIN, TAB, V, VO, VS, WIDTH, WS, append, attn, built, cache,  # noqa: F401
+                              gather)
 
 ROW = 6144                  # a fused f32 row: 4096 of q, 1024 of k, 1024 of v
 ARG, OK = pq.PQ_ERR_ARG, pq.PQ_ERR_DEVICE
@@ -72,6 +73,37 @@ def test_attention_into_other_columns_is_taken(no_gpu):
 ])
 def test_attention_into_the_same_columns_is_refused(kw):
     assert attn(cache(), **kw) == ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(row_start=OUT), dict(row_start=OUT + 4 * (4 * WIDTH - 4)), dict(row_start=K + 64), dict(row_start=VS + 4), dict(row_start=V),
+    dict(rope_cos=OUT + 64), dict(rope_sin=OUT - 4 * 64 * 1023), dict(rope_sin=K), dict(rope_cos=VS),
+    dict(q=K, q_out=OUT), dict(q=V + 4096, q_out=OUT), dict(q=VS, q_out=OUT),
+])
+def test_append_writes_nothing_that_it_reads(kw):
+    assert append(cache(), **kw) == ARG
+
+
+@pytest.mark.parametrize("kw", [dict(v=K), dict(v=K + 64 * 8 * 64 * 128 - 16), dict(vs=KS), dict(ks=V), dict(vs=K + 16), dict(table=K),
+                                dict(len_=KS + 4), dict(table=VS)])
+def test_append_writes_each_buffer_of_the_cache_once(kw):
+    assert append(cache(**kw)) == ARG
+
+
+def test_readers_may_share_buffers_of_the_cache(no_gpu):
+    assert attn(cache(v=K, vs=KS)) == gather(cache(v=K, vs=KS)) == OK
+    assert append(cache(), rope_sin=COS, k=KO, v=KO) == OK
+    assert append(cache(), row_start=QKV) == OK
+
+
+@pytest.mark.parametrize("kw", [dict(row_start=OUT), dict(row_start=WS + 1024), dict(row_start=OUT - 16), dict(ws=ROWS, row_start=ROWS + 64)])
+def test_attention_writes_nothing_that_it_reads(kw):
+    assert attn(cache(), **kw) == ARG
+
+
+@pytest.mark.parametrize("kw", [dict(row_start=KO), dict(row_start=VO + 4 * 1024)])
+def test_gather_writes_nothing_that_it_reads(kw):
+    assert gather(cache(), **kw) == ARG
 
 
 @pytest.mark.gpu
