@@ -208,7 +208,8 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
     const int64_t w = (int64_t)c.n_kv * c.d;
     if ((st = check_rows(k_out, ldk, w, n_rows, eb)) || (st = check_rows(v_out, ldv, w, n_rows, eb))) return st;
     if (touches_cache(k_out, rows_bytes(ldk, w, n_rows, eb), c, row_start) ||
-        touches_cache(v_out, rows_bytes(ldv, w, n_rows, eb), c, row_start))
+        touches_cache(v_out, rows_bytes(ldv, w, n_rows, eb), c, row_start) ||
+        rows_overlap({k_out, ldk, w, n_rows, eb}, {v_out, ldv, w, n_rows, eb}))
         return PQ_ERR_ARG;
     if ((st = check_gb300())) return st;
     if (n_rows == 0) return PQ_OK;

@@ -106,6 +106,19 @@ def test_gather_writes_nothing_that_it_reads(kw):
     assert gather(cache(), **kw) == ARG
 
 
+@pytest.mark.parametrize("kw", [
+    dict(v_out=KO), dict(v_out=KO + 64), dict(v_out=KO + 4 * 3 * 1024), dict(v_out=KO - 4 * 1000),
+    dict(ldk=2048, ldv=2048, v_out=KO + 4 * 1020), dict(ldk=2048, v_out=KO + 4 * 1024),
+])
+def test_gather_into_overlapping_rows_is_refused(kw):
+    assert gather(cache(), **kw) == ARG
+
+
+def test_gather_into_columns_of_one_buffer_is_taken(no_gpu):
+    assert gather(cache(), ldk=2048, ldv=2048, v_out=KO + 4 * 1024) == OK
+    assert gather(cache(), v_out=KO + 4 * 4 * 1024) == OK
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("news", [None, [40, 3, 70]])
