@@ -298,7 +298,8 @@ int pq_gemv_noalloc(pq_fmt fmt, const void *w_blocks, int n_out, int k,
  * Rows.  A call's rows (the new tokens, or the queries) lie sequence by
  * sequence: those of sequence s are rows row_start[s] .. row_start[s+1]-1
  * (device int32 [n_seq+1], from 0 to n_rows, not decreasing).  row_start may
- * be NULL: one row per sequence, n_rows == n_seq.  Row i of the m rows of
+ * be NULL: one row per sequence, n_rows == n_seq.  Without rows (n_rows 0) a call
+ * does nothing, and the rows' pointers may be NULL.  Row i of the m rows of
  * sequence s is the token at position len[s] - m + i.  A position below 0, or
  * one whose page the table does not have, is in no cache: such a token is not
  * written, not visible, and reads as zeros.  So an idle slot of a batch has

@@ -12,7 +12,7 @@ namespace {
 
 bool span_overlaps(const void *a, int64_t na, const void *b, int64_t nb) {
     const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
-    return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+    return na > 0 && nb > 0 && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
 }
 
 int check_gb300(const DeviceInfo **out = nullptr) {
@@ -46,9 +46,9 @@ int check_cache(const pq_kv_cache *c, const int *row_start, int n_rows) {
     return PQ_OK;
 }
 
-// Rows of `width` elements, `ld` apart.
+// Rows of `width` elements, `ld` apart; without rows no address either.
 int check_rows(const void *p, int64_t ld, int64_t width, int n_rows, int eb) {
-    if (!p || ld < width) return PQ_ERR_ARG;
+    if ((!p && n_rows > 0) || ld < width) return PQ_ERR_ARG;
     if (width > (INT64_C(1) << 24) || ld > kMost / (n_rows > 0 ? n_rows : 1)) return PQ_ERR_SIZE;
     if ((uintptr_t)p % 16 || ld * eb % 16) return PQ_ERR_ALIGN;
     return PQ_OK;
