@@ -189,7 +189,7 @@ int pq_kv_append(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
     a.ldqo = ldqo;
     a.cos = rope_cos;
     a.sin = rope_sin;
-    a.n_q = n_q;
+    a.n_q = q ? n_q : 0;
     a.n_pos = n_pos;
     a.rot = rot;
     a.pair = rope_mode == PQ_ROPE_PAIR;

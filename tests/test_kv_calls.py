@@ -42,3 +42,23 @@ def test_no_rows_from_empty_tensors(cuda_ok):
     assert pq.pq_attn(h, rs, 0, "f32", none, 64, 1, 1.0, 0, 0, none, 64, ws, ws.numel()) == 0
     torch.cuda.synchronize()
     assert all(torch.equal(a.view(torch.uint8), t[n].view(torch.uint8)) for a, n in zip(before, ("k", "v", "ks", "vs")))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows_given", [False, True])
+@pytest.mark.parametrize("n_q", [0, 7, 1 << 30, -5])
+def test_without_q_its_head_count_does_not_matter(n_q, rows_given, cuda_ok):
+    import torch
+
+    import kvref
+    from test_gpu_kv_cache import upload
+    c = kvref.Cache(2, [5, 36], 2, 16, 64, seed=1)
+    rs = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda") if rows_given else None
+    x = torch.randn(2, 256, device="cuda")
+    got = []
+    for n in (0, n_q):
+        t, h = upload(c)
+        pq.pq_kv_append(h, rs, 2, "f32", x, 256, x[:, 128:], 256, n_q=n)
+        torch.cuda.synchronize()
+        got.append([t[k] for k in ("k", "v", "ks", "vs")])
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*got))
