@@ -19,6 +19,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
+// Steps of a row whose loads are issued together: 4 for one column, else 2, the columns' sums taking the registers
+// (14336x4096, one column, 4 and 2: Q6_K 29.9 and 31.6 us, Q3_K 30.7 and 33.2, int8 17.5 and 22.8; four columns: Q6_K
+// 65.0 and 62.9, int8 41.6 and 35.5); Q2_K, whose codes are few, 4 for two columns too (32.5 and 35.2).
+template <int NB, int FMT = PQ_Q4_K> constexpr int kSteps = NB == 1 || (NB == 2 && FMT == PQ_Q2_K) ? 4 : 2;
+
 // Launched with programmatic dependent launch when the whole grid is resident
 // at once (at most one block per SM): the block may start while the previous
 // kernel on the stream finishes and waits for it before reading anything.
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(kThreads)
     float acc[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[b] = 0.f;
-#pragma unroll 2
+#pragma unroll kSteps<NB>
     for (int blk = 0; blk < nb; ++blk) {
         const uint8_t *bp = wr + (int64_t)blk * 210;
         const float d = h2f(ldg_u16(bp + 208));
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kThreads)
     float acc[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[b] = 0.f;
-#pragma unroll 2
+#pragma unroll kSteps<NB, FMT>
     for (int blk = 0; blk < nb; ++blk) {
         float wv[8];
         kfamily_lane<FMT>(wr + (int64_t)blk * BB, lane, wv);
@@ -286,6 +291,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[b] = 0.f;
     if ((k & 3) == 0) {
+#pragma unroll kSteps<NB>
         for (int i = 4 * lane; i < k; i += 128) {
             const uint32_t q = ldg_u32(wr + i);
             const float q0 = (float)(int8_t)(q & 0xff), q1 = (float)(int8_t)((q >> 8) & 0xff);
@@ -329,6 +335,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[b] = 0.f;
     if ((k & 7) == 0) {
+#pragma unroll kSteps<NB>
         for (int i = 8 * lane; i < k; i += 256) {
             const uint32_t q = ldg_u32(wr + i / 2);
             float wv[8];
