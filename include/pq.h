@@ -280,7 +280,7 @@ int pq_gemv_noalloc(pq_fmt fmt, const void *w_blocks, int n_out, int k,
  * (grouped-query attention over a cache of keys and values: PESTI README,
  * "Conformance"; ember pull request, attention.rs).  The cache holds int8
  * codes with one f32 scale per page and kv head, for K and for V separately:
- * a quarter of the bytes of an f32 cache, plus 8 / (page * d) bytes per value.
+ * a quarter of the bytes of an f32 cache, plus 4 / (page * d) bytes per value.
  *
  *   k, v              device int8 [n_pages][n_kv][page][d], 16-byte aligned;
  *                     value = scale * code
@@ -376,12 +376,16 @@ int pq_kv_gather(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_
  *   ws    device, 16-byte aligned, at least pq_attn_ws_bytes(...) bytes; what it
  *         holds before and after a call does not matter.  Calls that may
  *         overlap on the GPU need one each.
- * Accumulation in f32; q (scaled per row by a power of two) and the softmax
- * weights (times their page's V scale over a power of two that follows the row's
- * largest such product) enter the tensor cores as fp16, f32 rows' as fp16 pairs,
- * the codes exactly.  So a weight that counts is off by 2^-12 of itself (as a pair
- * by 2^-22), whatever the pages' scales are beside each other, and what is lost of the
- * smallest ones stays below 2^-24 of the largest product for each token.  Deterministic.
+ * Sums, maxima and scores in f32.  At head sizes 64 and 128 q (scaled per row by
+ * a power of two) and the softmax weights (times their page's V scale, over a power
+ * of two that follows the row's largest such product) enter the tensor cores as
+ * fp16, the codes exactly: q and the weights of f32 rows as fp16 pairs, the
+ * weights of f16 rows as pairs in calls of up to 32 rows (new tokens times n_q / n_kv,
+ * the mean) per sequence and singly in longer ones, of bf16 rows singly.  So a weight is off
+ * by 2^-12 of itself (as a pair by 2^-22), whatever the pages' scales are beside
+ * each other, or, the smallest ones, by 2^-25 of the row's largest product.  A V scale
+ * below 2^-126 counts as 0, one of 2^122 or more (its codes would overflow f32) as NaN.
+ * Other head sizes: all in f32.  Deterministic.
  */
 int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt,
             const void *q, long long ldq, int n_q, float scale, int window, int n_sink,

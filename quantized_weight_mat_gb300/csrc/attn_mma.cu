@@ -10,7 +10,8 @@
 // one token's code is loaded by exactly one thread.  Operands are exact where
 // they can be: int8 codes become fp16 by a byte permute and one subtraction
 // (0x6400 | (code + 128) is 1152 + code); q is scaled per row by a power of
-// two into fp16's range (one fp16 for 16-bit rows, an fp16 pair for f32 rows).
+// two, its largest element to 2^9..2^10 (16-bit rows as one fp16, exact but for bf16 elements 2^26 below
+// the row's largest; f32 rows as a pair, 2^-21 of each element or 2^-34 of the largest).
 // The softmax weights enter in fp16 for bf16 rows (their 11 bits lie far below
 // the output's 8) and as an fp16 pair for f16 and f32 rows (one fp16 would add half
 // as much again to f16's own rounding, and the loads hide the second product), already times

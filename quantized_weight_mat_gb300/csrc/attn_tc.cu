@@ -5,8 +5,8 @@
 // side: 128 rows by 128 tokens per product,
 //     S = q' K^T     A = q' (fp16, shared memory), B = K's codes (fp16, K-major)
 //     O += P V       A = P (fp16, tensor memory, over S), B = V's codes (MN-major)
-// q' is q scaled per row by a power of two (exact for bf16 and f16), codes are
-// exact in fp16.  A CTA takes 256 rows of one sequence and kv head, as two
+// q' is q scaled per row by a power of two, its largest element to 2^9..2^10 (exact, but for bf16 elements 2^26 below
+// the row's largest, which lose last bits), codes are exact in fp16.  A CTA takes 256 rows of one sequence and kv head, as two
 // halves whose products and softmaxes alternate, so that both share one
 // conversion of each K and V tile from 8 bits.  P lies over the S it came from.
 //
@@ -16,8 +16,8 @@
 // weights (fma, exponential, sum, packing: 2.5 instructions each, and the
 // reads of tensor memory), the products after it 512 + 512, the hand-overs
 // 400.  2048 rows of 32 heads over 10240 tokens (8 kv heads of 128) take
-// 249 us, 1.2 PFLOP/s of the 1.93 that a large bf16 product reaches; 4 prompts of
-// 1000 to 4096 tokens with a window of 1024 (14 heads of 64 over 2) 86 us, where
+// 248 us, 1.2 PFLOP/s of the 1.93 that a large bf16 product reaches; 4 prompts of
+// 1000 to 4096 tokens with a window of 1024 (14 heads of 64 over 2) 83 us, where
 // the items' starts and ends and the masked tiles cost as much as the rest.
 // Measured and not taken: halves of a tile's tokens as products of their own
 // (S: 305 us, P V: 285), with 128 weights held before any is stored 282.
@@ -42,8 +42,12 @@
 // The running maximum and R lag as in the decode kernel, so O
 // is rescaled (by its own row's thread) only now and then: when a
 // row's weights of 64 tokens, with or without the scales, sum to more than 2^15, which keeps each inside
-// fp16 and needs no maximum per element.  P is rounded to fp16 (11 bits, as
-// f16 rows are; bf16 rows have 8; below 2^-14 of R an absolute 2^-25 of it), the sum l is taken of the weights before.
+// fp16 and needs no maximum per element.  P is rounded to fp16: 11 bits, below
+// 2^-14 of R an absolute 2^-25 of it; the sum l is taken of the weights before.
+// bf16 rows, which have 8 bits, do not see it (1.66e-3 of the output off against 64 bits, 1.65e-3
+// by the output's own rounding).  f16 rows do (2.9e-4 against 2.1e-4): as pairs of fp16, as the
+// decode kernel takes them, they are at 2.1e-4, but the second P V and the packing cost
+// 2048 rows over 10240 tokens 317 us instead of 248 and the windowed prompts 97 instead of 83.
 // Tiles at an edge of some row's view take the same step with a mask; tiles
 // with missing pages, with scales that are no ordinary positive numbers, or
 // with maxima past 2^20 (where the V scale would be lost beside it) a slower one.

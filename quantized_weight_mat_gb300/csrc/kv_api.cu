@@ -264,8 +264,9 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
     const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
     cudaError_t e;
     // 16-bit rows: the wide kernel (256 rows at a time) from more than 32 rows per sequence and kv head. 16 sequences
-    // of 2048 tokens, head size 128: 32 rows 42.7 us (narrow) against 49.2 (wide), 64 rows 69.0 against 52.0; head size
-    // 64: 28 rows 13.8 against 18.1, 56 rows 18.9 against 18.1. f32 rows keep the pair of fp16 that only the narrow one has.
+    // of 2048 tokens, bf16, head size 128: 16 rows 30.1 us (narrow) against 41.9 (wide), 32 rows 43.3 against 42.4, 64 rows
+    // 69.7 against 43.9; head size 64: 28 rows 13.7 against 18.1, 56 rows 18.8 against 18.3. f32 rows keep the pair of fp16
+    // for q and for the weights that only the narrow one has.
     if (c.d != 64 && c.d != 128) e = launch_attn_generic((int)dt, a, stream);
     else if (dt != PQ_F32 && rows > 32) e = launch_attn_tc((int)dt, a, stream, *dev);
     else e = launch_attn_mma((int)dt, a, rows, stream, *dev);
