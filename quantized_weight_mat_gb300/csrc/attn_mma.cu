@@ -28,7 +28,7 @@
 // units, two elements of two tokens (V): the byte permutes of the conversion
 // sort them, so the transposition of V costs nothing.
 //
-// 64 sequences of 2560 tokens (32 heads over 8 of 128, bf16) take 61 us, 5.5 TB/s
+// 64 sequences of 2560 tokens (32 heads over 8 of 128, bf16) take 61.6 us, 5.4 TB/s
 // of K and V where the same loads without the arithmetic take 59; one sequence of 131072
 // 54, of 4096 11.7, of which 4.5 pass before the first tile is there (lengths,
 // table, TMA) and 2.5 in the second kernel.  More warps of 16 tokens each: 78 us against 64.

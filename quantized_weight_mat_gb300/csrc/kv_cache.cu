@@ -174,7 +174,7 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs &p, int b, int
 // maximum and the codes they wait in registers (SINGLE: one row per sequence,
 // one unit a thread, one warp a block) or as f32 in shared memory.
 // 8192 new tokens of 8 kv heads of 128 with the 32 query heads' rotation take
-// 49.6 us (bf16; 20.6 without q), where the bytes alone need 27: a block's phases
+// 49.2 us (bf16; 20.4 without q), where the bytes alone need 27: a block's phases
 // (load, maximum, codes) hide each other's latency only across the 6 blocks of an SM.
 // Single tokens are bound by the chain of dependent loads (length, page, scale):
 // 2.5 us for one sequence, 3.8 for 128.
