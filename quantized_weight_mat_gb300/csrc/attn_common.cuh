@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// (sx, sy) += (x, y), each rounded to nearest.
+__device__ __forceinline__ void add2(float &sx, float &sy, float x, float y) {
+    asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
+        : "+f"(sx), "+f"(sy)
+        : "f"(x), "f"(y));
+}
 // Two biased codes (code + 128) of w, chosen by the permutation SEL, as exact fp16.
 template <uint32_t SEL> __device__ __forceinline__ uint32_t codes2(uint32_t w) {
     const uint32_t v = __byte_perm(w, 0x64646464u, SEL), bias = 0x64806480u;      // 1152

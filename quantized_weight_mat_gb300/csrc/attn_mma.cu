@@ -5,7 +5,8 @@
 // the products go to the tensor cores and the loads to TMA.  Softmax in one
 // pass (running maximum m and sum l of exp2(s - m)):
 //     S = K q'      (16 tokens x 8 rows per mma.sync m16n8k16)
-//     O += V^T P    (16 elements x 8 rows)
+//     O += V^T P    (16 elements x 8 rows; f32 rows' tile by tile, see below: over 131072 tokens the products' own sums
+//                    left O 2.5e-5 short, now 9e-7 off in all; 2048 rows over 10240 tokens 2077 us -> 2202)
 // with K and V as the A operands, so that rows fill the narrow side (N = 8) and
 // one token's code is loaded by exactly one thread.  Operands are exact where
 // they can be: int8 codes become fp16 by a byte permute and one subtraction
@@ -524,18 +525,35 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int i = 0; i < 2; ++i) ldsm4t(vt + 16 * i * D + ((uint32_t)(32 * c2) ^ lofs), w[c2][i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[c2][i][e] ^= 0x80808080u;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 2; ++e) {
+                    // Products cut their sums off instead of rounding them: about 2^-25 of O each, always towards zero. f32 rows'
+                    // start from zero in every tile and are added to O with a rounding.
+                    float part[NT][4];
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) part[x][r] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
                         // row g of the fragment is element 2g of the chunk, row g + 8 element 2g + 1
                         const uint32_t lo = w[c2][i][2 * e], hi = w[c2][i][2 * e + 1];
                         const uint32_t a[4] = {codes2<0x4240>(lo), codes2<0x4341>(lo), codes2<0x4240>(hi), codes2<0x4341>(hi)};
 #pragma unroll
                         for (int x = 0; x < NT; ++x) {
-                            mma(o[x][2 * c2 + e], a, ph[i][x][0], ph[i][x][1]);
-                            if constexpr (WPAIR) mma(o[x][2 * c2 + e], a, pl[i][x][0], pl[i][x][1]);
+                            float(&to)[4] = PAIR ? part[x] : o[x][2 * c2 + e];
+                            mma(to, a, ph[i][x][0], ph[i][x][1]);
+                            if constexpr (WPAIR) mma(to, a, pl[i][x][0], pl[i][x][1]);
+                        }
+                    }
+                    if constexpr (PAIR) {
+#pragma unroll
+                        for (int x = 0; x < NT; ++x) {
+                            add2(o[x][2 * c2 + e][0], o[x][2 * c2 + e][1], part[x][0], part[x][1]);
+                            add2(o[x][2 * c2 + e][2], o[x][2 * c2 + e][3], part[x][2], part[x][3]);
                         }
                     }
                 }

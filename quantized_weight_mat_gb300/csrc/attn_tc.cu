@@ -96,17 +96,12 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
-// (x, y) * f + a, and sums of pairs.
+// (x, y) * f + a.
 __device__ __forceinline__ void fma2(uint32_t &x, uint32_t &y, float f, float a) {
     asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n mov.b64 r, {%3, %3};\n"
         " fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}"
         : "+r"(x), "+r"(y)
         : "f"(f), "f"(a));
-}
-__device__ __forceinline__ void add2(float &sx, float &sy, float x, float y) {
-    asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
-        : "+f"(sx), "+f"(sy)
-        : "f"(x), "f"(y));
 }
 
 // Bits of the f32 with the value of a positive 16-bit pattern (both order as their bits do).
