@@ -31,7 +31,7 @@
 //
 // 64 sequences of 2560 tokens (32 heads over 8 of 128, bf16) take 61.6 us, 5.4 TB/s
 // of K and V where the same loads without the arithmetic take 59; one sequence of 131072
-// 54, of 4096 11.7, of which 4.5 pass before the first tile is there (lengths,
+// 54, of 4096 (f32) 12.0, of which 4.5 pass before the first tile is there (lengths,
 // table, TMA) and 2.5 in the second kernel.  More warps of 16 tokens each: 78 us against 64.
 //
 // Pipeline: warp 4 walks the CTA's units (the other warps get each item from it
@@ -53,7 +53,7 @@ namespace {
 constexpr int kConsumers = 4;                // warps, 32 tokens of a tile each
 constexpr int kThreads = 32 * (kConsumers + 2);
 constexpr int kItemCost = 2;                 // places of an item beside its units (64 ragged sequences: 1: 70.7 us, 2: 65.6, 3: 67.4)
-constexpr int kLeast = 2;                    // places of a CTA (one row over 4096 tokens: 1: 12.7 us, 2: 11.7, 3: 12.7; over 512: 8.6, 9.3, 10.0)
+constexpr int kLeast = 2;                    // places of a CTA (one f32 row over 4096 tokens, before its sums were added up by tiles: 1: 12.7 us, 2: 11.7, 3: 12.7; over 512: 8.6, 9.3, 10.0)
 constexpr int kItems = 8;                    // items that the walking warp may be ahead (more than the tiles it looks up at a time)
 
 template <int D> __host__ __device__ constexpr int tile_bytes() { return KT * D; }
@@ -80,7 +80,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 // n + add for a small whole number n, without the conversion instruction (a quarter of the rate of additions, and the
-// exponentials' unit: 2048 f32 rows over 10240 tokens 2108 us with it, 2077 without).
+// exponentials' unit: 2048 f32 rows over 10240 tokens 31 us more with it).
 __device__ __forceinline__ float small_float(int n, float add) { return __int_as_float(0x4b400000 + n) - (12582912.f - add); }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
