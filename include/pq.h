@@ -395,6 +395,130 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
  * (0 for sizes pq_attn rejects). */
 size_t pq_attn_ws_bytes(int n_q, int n_kv, int d);
 
+/*
+ * The same attention with scores that are capped or biased by distance, and
+ * with rows that see less or more than what lies before them:
+ *   x_t = scale * (q[r][h] . k_t)
+ *   x_t = cap * tanh(x_t / cap)                when cap > 0 (0: no cap)
+ *   x_t = x_t - slope[h] * |pos - t|           with slope
+ * over the tokens t of the row's sequence with t < len, t >= first[r] (with
+ * first) and
+ *   t < prefix[r] (with prefix)   or   what pq_attn shows the row.
+ * So first[r] is where the row's document begins when several lie in one
+ * sequence, and prefix[r] the end of what all rows see, before them or after.
+ * A row at a position below 0 sees nothing.  window and n_sink count from the
+ * row's position and the sequence's first token, as in pq_attn.
+ *   cap     0, or from 2^-60 to 2^60
+ *   slope   device f32 [n_q], or NULL
+ *   first, prefix  device int32 [n_rows], or NULL; any values, in any order
+ * mod is plain host memory, read during the call only; NULL, or one without
+ * any of the four, is pq_attn.  Everything else, the accuracy included, is as in
+ * pq_attn, but for the cap's own error: 2^-21 of a capped score in calls of f32
+ * rows, 2^-21 of the cap in the others; the bias is rounded to f32.  ws: at least pq_attn_mod_ws_bytes(...) bytes.
+ */
+typedef struct pq_score_mod {
+    float cap;
+    const float *slope;
+    const int *first;
+    const int *prefix;
+} pq_score_mod;
+
+int pq_attn_mod(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt,
+                const void *q, long long ldq, int n_q, float scale, int window, int n_sink, const pq_score_mod *mod,
+                void *out, long long ldo, void *ws, size_t ws_bytes, struct CUstream_st *stream);
+
+/* Workspace bytes for a pq_attn_mod call of up to n_rows rows of n_seq
+ * sequences (0 for sizes it rejects). */
+size_t pq_attn_mod_ws_bytes(int n_q, int n_kv, int d, int n_rows, int n_seq);
+
+/* ------------------------------------------------------------------------
+ * The pool of a paged cache's pages: sequences that share pages, room for new
+ * tokens, pages given back.
+ *
+ * One pool serves all layers: their caches have the same n_pages, page size and
+ * table, so a page number means a page in each of them.
+ *
+ *   refs   device int32 [n_pages], 16-byte aligned: how many table entries name
+ *          the page; a page at 0 or below is free.  A program that keeps pages
+ *          without a sequence (a prompt's, for the next one that begins like
+ *          it) counts itself in.
+ *   table  device int32 [n_seq][table_ld], len device int32 [n_seq]: those of
+ *          the caches
+ * An empty pool is refs 0, table -1, len 0.  Entries outside [0, n_pages) name
+ * no page and are never followed; negative lengths count as 0.  A sequence may
+ * hold pages behind its len (room for tokens that are not there yet).
+ * n_seq is at most 65536, n_seq * table_ld at most 2^28, n_pages at most 2^28.
+ *
+ * All four calls run on the device from what lies there, asynchronously on
+ * `stream`, and can be captured in a graph.  Their results are the same
+ * whatever the order in which the GPU works.  Lists of the caller's are
+ * device memory; lists and status overlap neither the pool nor the workspace nor each
+ * other's output (PQ_ERR_ARG).  ws: 16-byte aligned, at least
+ * pq_kv_pool_ws_bytes(pool) bytes; what it holds before and after a call does
+ * not matter.  Calls that may overlap on the GPU need a workspace, and a pool, each.
+ */
+typedef struct pq_kv_pool {
+    int *refs, *table, *len;
+    int n_pages, page, n_seq, table_ld;
+} pq_kv_pool;
+
+size_t pq_kv_pool_ws_bytes(const pq_kv_pool *pool);      /* 0 for a pool that the calls reject */
+
+/*
+ * Sequence to[i] becomes what sequence from[i] was before the call, for all
+ * i < n at once: its first m = min(len, tokens[i]) tokens (tokens NULL: all of
+ * them), in the same pages.  What to[i] held before is given back; room behind
+ * the m tokens is not shared.  So a beam search's step is one call with each
+ * beam's parent.  Pairs with a number outside [0, n_seq) are passed over; of pairs with
+ * the same `to` the first counts.  from[i] == to[i] cuts a sequence to m tokens.
+ *   from, to, tokens  device int32 [n], n at most n_seq
+ * A page that tokens are appended to must be held once: pq_kv_reserve sees to it.
+ */
+int pq_kv_fork(const pq_kv_pool *pool, int n, const int *from, const int *to, const int *tokens, void *ws, size_t ws_bytes,
+               struct CUstream_st *stream);
+
+/*
+ * Room for n_new[s] more tokens in every sequence s (device int32 [n_seq];
+ * 0 or less: nothing), before they are appended: blocks len / page to
+ * (len + n_new - 1) / page of its row get a page that nobody else holds.
+ * A block without a page gets a free one; one whose page others hold too gets
+ * a free one and the codes and scales of the sequence's tokens in it, in all
+ * layers (codes behind them stay as they were).  When all who hold a page
+ * write to it in this call, the lowest of them keeps it.  Free pages are
+ * given out from the lowest number up, in the order of sequences and blocks.
+ * len is left to the caller.
+ *   caches  host array of n_caches handles (up to 1024; may be NULL with 0,
+ *           for a pool in which no page with tokens is shared), with the pool's n_pages and
+ *           page; their table and len are not looked at
+ *   status  device int32 [2]: free pages that lacked, and sequences whose row
+ *           is too short.  Both 0: done.  Else nothing has changed.
+ */
+int pq_kv_reserve(const pq_kv_pool *pool, const pq_kv_cache *caches, int n_caches, const int *n_new, int *status, void *ws,
+                  size_t ws_bytes, struct CUstream_st *stream);
+
+/*
+ * Give back the pages of sequence seq[i] (seq NULL: i) whose tokens all lie in
+ * begin[i] .. end[i] - 1 (begin NULL: 0; below 0: 0), i < n; their entries become -1.  An end
+ * at len or behind it (or end NULL) means all that follows, room included, and
+ * sets len to begin if that is less.  So: begin and end NULL frees sequences,
+ * begin alone takes tokens back, end alone forgets what a sliding window has
+ * left (of an end before len only whole pages go, and len stays).  An empty
+ * range does nothing; numbers outside [0, n_seq) are passed over; of equal
+ * numbers the first counts.
+ *   seq, begin, end  device int32 [n], n at most n_seq
+ */
+int pq_kv_free(const pq_kv_pool *pool, int n, const int *seq, const int *begin, const int *end, struct CUstream_st *stream);
+
+/*
+ * Move the pages in use to the lowest numbers: with U of them, the i-th one
+ * numbered U or above (from below) goes to the i-th free page below U, its
+ * codes and scales in all layers; refs and table follow.
+ *   moved   device int32 [n_pages]: each page's new number, -1 for a free one; may be NULL
+ *   n_used  device int32 [1]: U
+ */
+int pq_kv_compact(const pq_kv_pool *pool, const pq_kv_cache *caches, int n_caches, int *moved, int *n_used, void *ws,
+                  size_t ws_bytes, struct CUstream_st *stream);
+
 #ifdef __cplusplus
 }
 #endif

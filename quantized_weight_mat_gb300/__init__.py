@@ -36,7 +36,9 @@ EXPORTS = ("pq_gemv", "pq_dequant", "pq_weight_bytes", "pq_strerror",
            "pq_gemv_kernel", "pq_gemv_choice", "pq_gemv_launches", "pq_wait_timeouts",
            "pq_set_weight_prefetch", "pq_gemv_noalloc", "pq_selftest_wait_timeout",
            "pq_gemv_bias", "pq_gemv_swiglu",
-           "pq_kv_append", "pq_kv_gather", "pq_attn", "pq_attn_ws_bytes")
+           "pq_kv_append", "pq_kv_gather", "pq_attn", "pq_attn_ws_bytes",
+           "pq_attn_mod", "pq_attn_mod_ws_bytes", "pq_kv_pool_ws_bytes", "pq_kv_fork", "pq_kv_reserve", "pq_kv_free",
+           "pq_kv_compact")
 
 _lock = threading.Lock()
 _lib = None
@@ -48,6 +50,17 @@ class KVCache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("len", ctypes.c_void_p),
                 ("n_pages", ctypes.c_int), ("n_kv", ctypes.c_int), ("page", ctypes.c_int), ("d", ctypes.c_int),
                 ("n_seq", ctypes.c_int), ("table_ld", ctypes.c_int)]
+
+
+class ScoreMod(ctypes.Structure):
+    """``pq_score_mod`` of include/pq.h; made by ``pq_score_mod``."""
+    _fields_ = [("cap", ctypes.c_float), ("slope", ctypes.c_void_p), ("first", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
+class KVPool(ctypes.Structure):
+    """``pq_kv_pool`` of include/pq.h; made by ``pq_kv_pool``."""
+    _fields_ = [("refs", ctypes.c_void_p), ("table", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int), ("page", ctypes.c_int), ("n_seq", ctypes.c_int), ("table_ld", ctypes.c_int)]
 
 
 class PQError(RuntimeError):
@@ -101,6 +114,21 @@ def lib() -> ctypes.CDLL:
             L.pq_attn.restype = i32
             L.pq_attn_ws_bytes.argtypes = [i32, i32, i32]
             L.pq_attn_ws_bytes.restype = sz
+            mp, pp = ctypes.POINTER(ScoreMod), ctypes.POINTER(KVPool)
+            L.pq_attn_mod.argtypes = [cp, vp, i32, i32, vp, ll, i32, ctypes.c_float, i32, i32, mp, vp, ll, vp, sz, vp]
+            L.pq_attn_mod.restype = i32
+            L.pq_attn_mod_ws_bytes.argtypes = [i32, i32, i32, i32, i32]
+            L.pq_attn_mod_ws_bytes.restype = sz
+            L.pq_kv_pool_ws_bytes.argtypes = [pp]
+            L.pq_kv_pool_ws_bytes.restype = sz
+            L.pq_kv_fork.argtypes = [pp, i32, vp, vp, vp, vp, sz, vp]
+            L.pq_kv_fork.restype = i32
+            L.pq_kv_reserve.argtypes = [pp, cp, i32, vp, vp, vp, sz, vp]
+            L.pq_kv_reserve.restype = i32
+            L.pq_kv_free.argtypes = [pp, i32, vp, vp, vp, vp]
+            L.pq_kv_free.restype = i32
+            L.pq_kv_compact.argtypes = [pp, cp, i32, vp, vp, vp, sz, vp]
+            L.pq_kv_compact.restype = i32
             L.pq_set_weight_prefetch.argtypes = [i32]
             L.pq_set_weight_prefetch.restype = i32
             _lib = L
@@ -279,3 +307,76 @@ def pq_attn(cache: KVCache, row_start, n_rows: int, dt, q, ldq: int, n_q: int, s
 
 def pq_attn_ws_bytes(n_q: int, n_kv: int, d: int) -> int:
     return int(lib().pq_attn_ws_bytes(int(n_q), int(n_kv), int(d)))
+
+
+def pq_score_mod(cap: float = 0.0, slope=None, first=None, prefix=None) -> ScoreMod:
+    """What pq_attn_mod does to scores and views (see include/pq.h); keeps the buffers it is given alive."""
+    m = ScoreMod(float(cap), _addr(slope), _addr(first), _addr(prefix))
+    m.buffers = (slope, first, prefix)
+    return m
+
+
+def pq_attn_mod(cache: KVCache, row_start, n_rows: int, dt, q, ldq: int, n_q: int, scale: float, window: int,
+                n_sink: int, mod: ScoreMod | None, out, ldo: int, ws, ws_bytes: int, stream=None, check: bool = True) -> int:
+    """pq_attn with capped scores, a bias by distance, rows' first tokens and prefixes that are seen whole."""
+    st = lib().pq_attn_mod(cache, _addr(row_start), n_rows, _dtype(dt), _addr(q), ldq, n_q, scale, window, n_sink, mod,
+                           _addr(out), ldo, _addr(ws), ws_bytes, _stream(stream))
+    if check and st:
+        raise PQError(st, "pq_attn_mod")
+    return st
+
+
+def pq_attn_mod_ws_bytes(n_q: int, n_kv: int, d: int, n_rows: int, n_seq: int) -> int:
+    return int(lib().pq_attn_mod_ws_bytes(int(n_q), int(n_kv), int(d), int(n_rows), int(n_seq)))
+
+
+def pq_kv_pool(refs, table, len_, n_pages: int, page: int, n_seq: int, table_ld: int) -> KVPool:
+    """Handle on the pool of a paged cache's pages (see include/pq.h); keeps the buffers it is given alive."""
+    p = KVPool(_addr(refs), _addr(table), _addr(len_), int(n_pages), int(page), int(n_seq), int(table_ld))
+    p.buffers = (refs, table, len_)
+    return p
+
+
+def pq_kv_layers(caches):
+    """The caches of a model's layers as the array that the pool's calls take; keeps the handles alive."""
+    layers = (KVCache * len(caches))(*caches)
+    layers.caches = tuple(caches)
+    return layers
+
+
+def pq_kv_pool_ws_bytes(pool: KVPool) -> int:
+    return int(lib().pq_kv_pool_ws_bytes(pool))
+
+
+def pq_kv_fork(pool: KVPool, n: int, from_, to, tokens, ws, ws_bytes: int, stream=None, check: bool = True) -> int:
+    """Sequence to[i] becomes the first tokens[i] (None: all) of what sequence from_[i] was, in the same pages."""
+    st = lib().pq_kv_fork(pool, n, _addr(from_), _addr(to), _addr(tokens), _addr(ws), ws_bytes, _stream(stream))
+    if check and st:
+        raise PQError(st, "pq_kv_fork")
+    return st
+
+
+def pq_kv_reserve(pool: KVPool, layers, n_new, status, ws, ws_bytes: int, stream=None, check: bool = True) -> int:
+    """Room for n_new[s] more tokens of every sequence, in pages that it alone holds; layers None: no codes are copied."""
+    st = lib().pq_kv_reserve(pool, layers, len(layers) if layers is not None else 0, _addr(n_new), _addr(status),
+                             _addr(ws), ws_bytes, _stream(stream))
+    if check and st:
+        raise PQError(st, "pq_kv_reserve")
+    return st
+
+
+def pq_kv_free(pool: KVPool, n: int, seq=None, begin=None, end=None, stream=None, check: bool = True) -> int:
+    """Give back the pages of tokens begin[i] .. end[i] - 1 of sequence seq[i] (None: i, from 0, to the end)."""
+    st = lib().pq_kv_free(pool, n, _addr(seq), _addr(begin), _addr(end), _stream(stream))
+    if check and st:
+        raise PQError(st, "pq_kv_free")
+    return st
+
+
+def pq_kv_compact(pool: KVPool, layers, moved, n_used, ws, ws_bytes: int, stream=None, check: bool = True) -> int:
+    """Move the pages in use to the lowest numbers, in all layers."""
+    st = lib().pq_kv_compact(pool, layers, len(layers) if layers is not None else 0, _addr(moved), _addr(n_used),
+                             _addr(ws), ws_bytes, _stream(stream))
+    if check and st:
+        raise PQError(st, "pq_kv_compact")
+    return st

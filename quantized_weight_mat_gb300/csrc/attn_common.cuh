@@ -4,6 +4,7 @@
 #include <cuda.h>
 
 #include "attn_sched.cuh"
+#include "attn_score.cuh"
 #include "pq_device.cuh"
 #include "pq_ptx.cuh"
 
@@ -12,7 +13,6 @@ namespace {
 
 constexpr int KT = 128;                      // tokens per tile
 constexpr int kGroups = KT / 16;             // groups of 16 tokens: always within one page
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMinExp = -200, kMaxExp = 125;   // of V scales: one that takes no part, and the largest
 constexpr int kLeastExp = -118;              // of a row's reference for V scales: 2^-(kLeastExp - 7) is a normal number, the smallest scale 2^-8 of it
 constexpr int kFarExp = 400;                 // differences of exponents beyond which nothing is left
@@ -24,11 +24,6 @@ struct TileMeta {
     int have[kGroups];                   // whether the group has a page
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // 2^e, 0 below the smallest normal number, 2^127 above it.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(min(max(e, -127), 127) + 127) << 23); }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {

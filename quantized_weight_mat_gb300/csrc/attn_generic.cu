@@ -10,15 +10,15 @@
 // the tokens of V one after the other, 16 sequences of 2048 tokens (20 query heads over
 // 4 of 80 elements) took 589 us, as it stands 85; 256 rows of one sequence took 1162 us and take 729.
 
-#include "kv_device.cuh"
+#include "attn_score.cuh"
 
 namespace pqk {
 namespace {
 
 constexpr int kWarps = 8, kMaxD = 256, kStride = 32 * kWarps;
-constexpr float kLog2e = 1.4426950408889634f;
 
-template <class T> __global__ void __launch_bounds__(32 * kWarps) attn_generic(AttnArgs p) {
+// MOD: scores and views of pq_attn_mod.
+template <class T, bool MOD> __global__ void __launch_bounds__(32 * kWarps) attn_generic(AttnArgs p) {
     __shared__ float qs[kMaxD], part[kWarps][kMaxD], part_m[kWarps], part_l[kWarps];
     __shared__ int sh;
     const KvView &c = p.c;
@@ -39,16 +39,24 @@ template <class T> __global__ void __launch_bounds__(32 * kWarps) attn_generic(A
     float m = -INFINITY, l = 0.f, acc[kMaxD / 32];
 #pragma unroll
     for (int i = 0; i < kMaxD / 32; ++i) acc[i] = 0.f;
-    const int end = (int)min((long long)pos + 1, (long long)c.table_ld * c.page);
+    RowView view = {0, 0};
+    float slope = 0.f;
+    if (MOD) {
+        if (pos >= 0) view = row_view(p, r, seq_len(c, s));
+        if (p.mod.slope) slope = p.mod.slope[h] * kLog2e;
+    }
+    const int end = (int)min((long long)max(pos + 1, view.prefix), (long long)c.table_ld * c.page);
     const int from = p.window > 0 ? max(0, pos - p.window + 1) : 0;      // first token of the window
-    for (int t0 = 32 * warp; t0 < end; t0 += kStride) {
-        if (t0 >= p.n_sink && t0 + 32 <= from) {                          // nothing visible: on to the window
+    const int keep = MOD ? max(p.n_sink, view.prefix) : p.n_sink;        // tokens before it that may be seen
+    for (int t0 = 32 * warp + (MOD ? view.first / kStride * kStride : 0); t0 < end; t0 += kStride) {
+        if (t0 >= keep && t0 + 32 <= from) {                          // nothing visible: on to the window
             t0 += (from / 32 * 32 - t0 + kStride - 1) / kStride * kStride - kStride;
             continue;
         }
         const int t = t0 + lane;
         const int pg = t < end ? page_of(c, s, t / c.page) : -1;
-        const bool see = pg >= 0 && (t >= from || t < p.n_sink);
+        const bool near = t >= from || t < p.n_sink;
+        const bool see = pg >= 0 && (MOD ? view.sees(t, pos, near) : near);
         float x = -INFINITY, vs = 0.f;
         long long vrow = 0;
         if (see) {
@@ -65,6 +73,10 @@ template <class T> __global__ void __launch_bounds__(32 * kWarps) attn_generic(A
             }
             const long long si = (long long)pg * c.n_kv + kvh;
             x = dot * c.k_scale[si];
+            if (MOD) {
+                if (p.mod.top > 0.f) x = capped<true>(x, p.mod);
+                x = fmaf(-slope, fabsf((float)(pos - t)), x);
+            }
             vs = c.v_scale[si];
             vrow = (long long)at;
         }
@@ -123,9 +135,11 @@ template <class T> __global__ void __launch_bounds__(32 * kWarps) attn_generic(A
 cudaError_t launch_attn_generic(int dt, const AttnArgs &a, cudaStream_t s) {
     const long long grid = (long long)a.c.n_rows * a.n_q;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    if (dt == PQ_F32) attn_generic<float><<<(unsigned)grid, 32 * kWarps, 0, s>>>(a);
-    else if (dt == PQ_F16) attn_generic<__half><<<(unsigned)grid, 32 * kWarps, 0, s>>>(a);
-    else attn_generic<__nv_bfloat16><<<(unsigned)grid, 32 * kWarps, 0, s>>>(a);
+    const bool mod = a.mod.any();
+    auto run = [&](auto kernel) { kernel<<<(unsigned)grid, 32 * kWarps, 0, s>>>(a); };
+    if (dt == PQ_F32) mod ? run(attn_generic<float, true>) : run(attn_generic<float, false>);
+    else if (dt == PQ_F16) mod ? run(attn_generic<__half, true>) : run(attn_generic<__half, false>);
+    else mod ? run(attn_generic<__nv_bfloat16, true>) : run(attn_generic<__nv_bfloat16, false>);
     return cudaGetLastError();
 }
 

@@ -1,0 +1,53 @@
+// Scores and views of pq_attn_mod: the cap, the bias by distance, a row's first token and prefix.
+#pragma once
+
+#include "kv_device.cuh"
+
+namespace pqk {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// x = score * log2 e -> cap * tanh(score / cap) * log2 e, from tanh y = 1 - 2 / (1 + e^2y): the exponential's and the
+// quotient's errors are absolute ones, cap * 2^-21 of the score, which 16-bit rows do not see. EXACT: a relative one, by
+// the Taylor series below y = 0.4 (its next term is 2^-24 of the sum there).
+template <bool EXACT> __device__ __forceinline__ float capped(float x, const AttnMod &m) {
+    const float y = x * m.to_unit;
+    const float far = fmaf(rcp(1.f + ex2(y * (2.f * kLog2e))), -2.f * m.top, m.top);
+    if (!EXACT) return far;
+    const float z = y * y;
+    float s = fmaf(z, -1382.f / 155925.f, 62.f / 2835.f);
+    s = fmaf(z, s, -17.f / 315.f);
+    s = fmaf(z, s, 2.f / 15.f);
+    s = fmaf(z, s, -1.f / 3.f);
+    s = fmaf(z * y, s, y) * m.top;
+    return fabsf(y) < 0.4f ? s : far;
+}
+
+// What a row sees beside what its position says: tokens from `first` on, and all below `prefix` (kept below len).
+struct RowView {
+    int first, prefix;
+    // near: causality aside, whether window and first tokens show it
+    __device__ __forceinline__ bool sees(int t, int pos, bool near) const { return t >= first && (t < prefix || (t <= pos && near)); }
+};
+// Of a row at a position of 0 or more.
+__device__ __forceinline__ RowView row_view(const AttnArgs &p, int r, int len) {
+    RowView v;
+    v.first = p.mod.first ? max(p.mod.first[r], 0) : 0;
+    v.prefix = p.mod.prefix ? min(max(p.mod.prefix[r], 0), len) : 0;
+    return v;
+}
+
+}  // namespace
+}  // namespace pqk

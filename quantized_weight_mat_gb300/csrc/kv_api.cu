@@ -4,31 +4,13 @@
 #include <cmath>
 #include <cstdint>
 
-#include "kv_internal.h"
+#include "kv_checks.h"
 
 using namespace pqk;
 
 namespace {
 
-bool span_overlaps(const void *a, int64_t na, const void *b, int64_t nb) {
-    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
-    return na > 0 && nb > 0 && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
-}
-
-int check_gb300(const DeviceInfo **out = nullptr) {
-    const DeviceInfo *dev = device_info();
-    if (!dev || dev->major != 10 || dev->minor != 3) return PQ_ERR_DEVICE;
-    if (out) *out = dev;
-    return PQ_OK;
-}
-
-constexpr int64_t kMost = INT64_C(1) << 40;
-
 int elem_bytes(int dt) { return dt == PQ_F32 ? 4 : dt == PQ_F16 || dt == PQ_BF16 ? 2 : 0; }
-
-bool head_size_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
-
-int64_t cache_bytes(const pq_kv_cache &c) { return (int64_t)c.n_pages * c.n_kv * c.page * c.d; }
 
 // The cache and the rows' places.
 int check_cache(const pq_kv_cache *c, const int *row_start, int n_rows) {
@@ -80,8 +62,6 @@ bool rows_overlap(const Rows &a, const Rows &b) {
     return k < b.n_rows && delta + k * ld < wa && delta + k * ld > -wb;
 }
 
-int64_t scale_bytes(const pq_kv_cache &c) { return 4 * (int64_t)c.n_pages * c.n_kv; }
-
 // What every entry reads of the places: table, lengths, row_start.
 bool touches_places(const void *p, int64_t bytes, const pq_kv_cache &c, const int *row_start) {
     return span_overlaps(p, bytes, c.table, 4 * (int64_t)c.n_seq * c.table_ld) ||
@@ -129,6 +109,74 @@ KvView view_of(const pq_kv_cache &c, const int *row_start, int n_rows) {
     v.table_ld = c.table_ld;
     v.n_rows = n_rows;
     return v;
+}
+
+// pq_attn, and pq_attn_mod where mod asks for something.
+int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt, const void *q, long long ldq, int n_q,
+           float scale, int window, int n_sink, const pq_score_mod *mod, void *out, long long ldo, void *ws, size_t ws_bytes,
+           struct CUstream_st *stream) {
+    int st = check_cache(cache, row_start, n_rows);
+    if (st) return st;
+    const int eb = elem_bytes((int)dt);
+    if (!eb) return PQ_ERR_DTYPE;
+    const pq_kv_cache &c = *cache;
+    if (n_q <= 0 || window < 0 || n_sink < 0 || !std::isfinite(scale) || !ws) return PQ_ERR_ARG;
+    if (n_q % c.n_kv) return PQ_ERR_LAYOUT;
+    const int64_t w = (int64_t)n_q * c.d;
+    if ((int64_t)n_rows * n_q > (INT64_C(1) << 30)) return PQ_ERR_SIZE;
+    if ((st = check_rows(q, ldq, w, n_rows, eb)) || (st = check_rows(out, ldo, w, n_rows, eb))) return st;
+    if ((uintptr_t)ws % 16) return PQ_ERR_ALIGN;
+    if (ws_bytes < (mod ? pq_attn_mod_ws_bytes(n_q, c.n_kv, c.d, n_rows, c.n_seq) : pq_attn_ws_bytes(n_q, c.n_kv, c.d))) return PQ_ERR_WS;
+    const int64_t ob = rows_bytes(ldo, w, n_rows, eb), qb = rows_bytes(ldq, w, n_rows, eb);
+    if (rows_overlap({out, ldo, w, n_rows, eb}, {q, ldq, w, n_rows, eb}) || touches_cache(out, ob, c, row_start) || span_overlaps(ws, (int64_t)ws_bytes, out, ob) ||
+        span_overlaps(ws, (int64_t)ws_bytes, q, qb) || touches_cache(ws, (int64_t)ws_bytes, c, row_start))
+        return PQ_ERR_ARG;
+    if (mod) {
+        if (mod->cap != 0.f && !(mod->cap >= 0x1p-60f && mod->cap <= 0x1p60f)) return PQ_ERR_ARG;
+        if ((uintptr_t)mod->slope % 4 || (uintptr_t)mod->first % 4 || (uintptr_t)mod->prefix % 4) return PQ_ERR_ALIGN;
+        const void *read[3] = {mod->slope, mod->first, mod->prefix};
+        const int64_t bytes[3] = {4 * (int64_t)n_q, 4 * (int64_t)n_rows, 4 * (int64_t)n_rows};
+        for (int i = 0; i < 3; ++i)
+            if (read[i] && (span_overlaps(read[i], bytes[i], out, ob) || span_overlaps(read[i], bytes[i], ws, (int64_t)ws_bytes)))
+                return PQ_ERR_ARG;
+    }
+    const DeviceInfo *dev = nullptr;
+    if ((st = check_gb300(&dev))) return st;
+    if (n_rows == 0) return PQ_OK;
+    AttnArgs a;
+    a.c = view_of(c, row_start, n_rows);
+    a.group = FastDiv(n_q / c.n_kv);
+    a.q = q;
+    a.out = out;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.scale = scale;
+    a.n_q = n_q;
+    // positions stay below 2^30 (check_cache), so larger values change nothing
+    a.window = window < (1 << 30) ? window : 1 << 30;
+    a.n_sink = n_sink < (1 << 30) ? n_sink : 1 << 30;
+    a.ws = static_cast<uint8_t *>(ws);
+    a.mod = AttnMod{};
+    if (mod) {
+        if (mod->cap > 0.f) {
+            a.mod.top = (float)(mod->cap * 1.4426950408889634);
+            a.mod.to_unit = (float)(1 / (mod->cap * 1.4426950408889634));
+        }
+        a.mod.slope = mod->slope;
+        a.mod.first = mod->first;
+        a.mod.prefix = mod->prefix;
+    }
+    const int group = a.group.d;
+    const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
+    cudaError_t e;
+    // 16-bit rows: the wide kernel (256 rows at a time) from more than 32 rows per sequence and kv head. 16 sequences
+    // of 2048 tokens, bf16, head size 128: 16 rows 30.1 us (narrow) against 41.9 (wide), 32 rows 43.3 against 42.4, 64 rows
+    // 69.7 against 43.9; head size 64: 28 rows 13.7 against 18.1, 56 rows 18.8 against 18.3. f32 rows keep the pair of fp16
+    // for q and for the weights that only the narrow one has.
+    if ((c.d != 64 && c.d != 128) || a.mod.any()) e = launch_attn_generic((int)dt, a, stream);
+    else if (dt != PQ_F32 && rows > 32) e = launch_attn_tc((int)dt, a, stream, *dev);
+    else e = launch_attn_mma((int)dt, a, rows, stream, *dev);
+    return e == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -228,49 +276,20 @@ size_t pq_attn_ws_bytes(int n_q, int n_kv, int d) {
 int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt, const void *q, long long ldq,
             int n_q, float scale, int window, int n_sink, void *out, long long ldo, void *ws, size_t ws_bytes,
             struct CUstream_st *stream) {
-    int st = check_cache(cache, row_start, n_rows);
-    if (st) return st;
-    const int eb = elem_bytes((int)dt);
-    if (!eb) return PQ_ERR_DTYPE;
-    const pq_kv_cache &c = *cache;
-    if (n_q <= 0 || window < 0 || n_sink < 0 || !std::isfinite(scale) || !ws) return PQ_ERR_ARG;
-    if (n_q % c.n_kv) return PQ_ERR_LAYOUT;
-    const int64_t w = (int64_t)n_q * c.d;
-    if ((int64_t)n_rows * n_q > (INT64_C(1) << 30)) return PQ_ERR_SIZE;
-    if ((st = check_rows(q, ldq, w, n_rows, eb)) || (st = check_rows(out, ldo, w, n_rows, eb))) return st;
-    if ((uintptr_t)ws % 16) return PQ_ERR_ALIGN;
-    if (ws_bytes < pq_attn_ws_bytes(n_q, c.n_kv, c.d)) return PQ_ERR_WS;
-    const int64_t ob = rows_bytes(ldo, w, n_rows, eb), qb = rows_bytes(ldq, w, n_rows, eb);
-    if (rows_overlap({out, ldo, w, n_rows, eb}, {q, ldq, w, n_rows, eb}) || touches_cache(out, ob, c, row_start) || span_overlaps(ws, (int64_t)ws_bytes, out, ob) ||
-        span_overlaps(ws, (int64_t)ws_bytes, q, qb) || touches_cache(ws, (int64_t)ws_bytes, c, row_start))
-        return PQ_ERR_ARG;
-    const DeviceInfo *dev = nullptr;
-    if ((st = check_gb300(&dev))) return st;
-    if (n_rows == 0) return PQ_OK;
-    AttnArgs a;
-    a.c = view_of(c, row_start, n_rows);
-    a.group = FastDiv(n_q / c.n_kv);
-    a.q = q;
-    a.out = out;
-    a.ldq = ldq;
-    a.ldo = ldo;
-    a.scale = scale;
-    a.n_q = n_q;
-    // positions stay below 2^30 (check_cache), so larger values change nothing
-    a.window = window < (1 << 30) ? window : 1 << 30;
-    a.n_sink = n_sink < (1 << 30) ? n_sink : 1 << 30;
-    a.ws = static_cast<uint8_t *>(ws);
-    const int group = a.group.d;
-    const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
-    cudaError_t e;
-    // 16-bit rows: the wide kernel (256 rows at a time) from more than 32 rows per sequence and kv head. 16 sequences
-    // of 2048 tokens, bf16, head size 128: 16 rows 30.1 us (narrow) against 41.9 (wide), 32 rows 43.3 against 42.4, 64 rows
-    // 69.7 against 43.9; head size 64: 28 rows 13.7 against 18.1, 56 rows 18.8 against 18.3. f32 rows keep the pair of fp16
-    // for q and for the weights that only the narrow one has.
-    if (c.d != 64 && c.d != 128) e = launch_attn_generic((int)dt, a, stream);
-    else if (dt != PQ_F32 && rows > 32) e = launch_attn_tc((int)dt, a, stream, *dev);
-    else e = launch_attn_mma((int)dt, a, rows, stream, *dev);
-    return e == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
+    return attend(cache, row_start, n_rows, dt, q, ldq, n_q, scale, window, n_sink, nullptr, out, ldo, ws, ws_bytes, stream);
+}
+
+size_t pq_attn_mod_ws_bytes(int n_q, int n_kv, int d, int n_rows, int n_seq) {
+    const size_t plain = pq_attn_ws_bytes(n_q, n_kv, d);
+    if (!plain || n_rows < 0 || n_seq <= 0 || (int64_t)n_rows * n_q > (INT64_C(1) << 30)) return 0;
+    return plain;
+}
+
+int pq_attn_mod(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt, const void *q, long long ldq,
+                int n_q, float scale, int window, int n_sink, const pq_score_mod *mod, void *out, long long ldo, void *ws,
+                size_t ws_bytes, struct CUstream_st *stream) {
+    static const pq_score_mod none = {};
+    return attend(cache, row_start, n_rows, dt, q, ldq, n_q, scale, window, n_sink, mod ? mod : &none, out, ldo, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -2,6 +2,8 @@
 // append, gather and attention kernels, and their launchers.
 #pragma once
 
+#include <vector_types.h>
+
 #include "pq_internal.h"
 
 namespace pqk {
@@ -42,8 +44,18 @@ struct KvAppendArgs {
     FastDiv units, per_row;      // d / 16, and n_q times that
 };
 
+// What pq_attn_mod does to scores and views; all empty in pq_attn.
+struct AttnMod {
+    float to_unit, top;        // a score times log2 e -> the cap's unit, and the cap times log2 e; 0: no cap
+    const float *slope;        // [n_q] or null
+    const int *first, *prefix; // [n_rows] or null
+    int2 *bounds;              // of row tiles with several rows: see attn_bounds
+    bool any() const { return top > 0.f || slope || first || prefix; }
+};
+
 struct AttnArgs {
     KvView c;
+    AttnMod mod;
     FastDiv group;             // query heads per kv head
     FastDiv grid;              // CTAs of the launch (set by the launcher)
     const void *q;

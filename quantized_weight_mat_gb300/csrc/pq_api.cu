@@ -269,7 +269,7 @@ const char *pq_strerror(int status) {
     case PQ_ERR_KERNEL: return "the requested kernel does not support this case";
     case PQ_ERR_DTYPE: return "unknown element type";
     case PQ_ERR_LAYOUT: return "head size, head counts, page size or rotated size not supported";
-    case PQ_ERR_WS: return "workspace too small (pq_attn_ws_bytes)";
+    case PQ_ERR_WS: return "workspace too small (pq_attn_ws_bytes, pq_attn_mod_ws_bytes, pq_kv_pool_ws_bytes)";
     }
     return "unknown status";
 }
