@@ -1,10 +1,10 @@
 // Shared by the attention kernels that bring tiles of K and V by TMA.
 #pragma once
 
+#include <climits>
 #include <cuda.h>
 
 #include "attn_sched.cuh"
-#include "attn_score.cuh"
 #include "pq_device.cuh"
 #include "pq_ptx.cuh"
 
@@ -174,6 +174,44 @@ template <class T, int D, int RT> __global__ void __launch_bounds__(256) attn_jo
         store4(static_cast<T *>(p.out) + (it.r0 + tk) * p.ldo + (long long)hd * D + 4 * col,
                make_float4(acc[r].x * inv, acc[r].y * inv, acc[r].z * inv, acc[r].w * inv));
     }
+}
+
+// What the rows of each row tile see at most: the first token of any, and the end of any's prefix (pq_attn_mod calls of
+// several rows per sequence, whose row tiles are counted by every CTA). A warp per row tile; sequences in blockIdx.x.
+constexpr int kBoundsWarps = 8, kBoundsSplit = 8;
+template <int RT> __global__ void __launch_bounds__(32 * kBoundsWarps) attn_bounds(AttnArgs p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int lane = threadIdx.x & 31, s = blockIdx.x;
+    int r0, m;
+    seq_rows(p.c, s, r0, m);
+    const int len = seq_len(p.c, s), rows = m * p.group.d;
+    for (int j = blockIdx.y * kBoundsWarps + (threadIdx.x >> 5); j * RT < rows; j += kBoundsSplit * kBoundsWarps) {
+        const int end = p.group.div(min((j + 1) * RT, rows) - 1);
+        int first = INT_MAX, prefix = 0;
+        for (int tok = p.group.div(j * RT) + lane; tok <= end; tok += 32)
+            if (len - m + tok >= 0) {
+                const RowView v = row_view(p, r0 + tok, len);
+                first = min(first, v.first);
+                prefix = max(prefix, v.prefix);
+            }
+        first = __reduce_min_sync(0xffffffffu, first);
+        prefix = __reduce_max_sync(0xffffffffu, prefix);
+        if (lane == 0) p.mod.bounds[bounds_at<RT>(p, s, r0, j)] = make_int2(first, prefix);
+    }
+}
+template <int RT> cudaError_t launch_bounds(const AttnArgs &a, cudaStream_t s) {
+    if (!a.c.row_start || !(a.mod.first || a.mod.prefix)) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.c.n_seq, kBoundsSplit);
+    cfg.blockDim = dim3(32 * kBoundsWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_bounds<RT>, a);
 }
 
 // Launches an attention kernel and the join of its parts, each so that it may be

@@ -1,0 +1,21 @@
+// The decode-step attention kernel with the scores and views of pq_attn_mod.
+
+#include "attn_mma.cuh"
+
+namespace pqk {
+
+unsigned attn_mma_mod_wait_timeouts(bool reset) {
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_wait_timeouts, sizeof(v)) != cudaSuccess) return 0;
+    if (reset) {
+        const unsigned z = 0;
+        cudaMemcpyToSymbol(g_wait_timeouts, &z, sizeof(z));
+    }
+    return v;
+}
+
+cudaError_t launch_attn_mma_mod(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
+    return launch_dt<true>(dt, a, rows, s, dev);
+}
+
+}  // namespace pqk

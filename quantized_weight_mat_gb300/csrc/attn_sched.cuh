@@ -14,7 +14,7 @@
 // sequence took 6 us of 52, and the last CTA's fence and counter 1 us of every split).
 #pragma once
 
-#include "kv_device.cuh"
+#include "attn_score.cuh"
 
 namespace pqk {
 
@@ -28,17 +28,46 @@ constexpr int kFewTiles = 4;
 struct RowTile {
     int rows;            // rows of the tile (the last one of a sequence may be short)
     int pos0, pos1;      // positions of the first and the last row's token
-    int sinks, w0;       // unit y is token tile y below sinks, else w0 + (y - sinks)
+    int s0, sinks, w0;   // unit y is token tile s0 + y below sinks, else w0 + (y - sinks)
     int units;           // at least 1, so that rows that see nothing are written
+    int first, prefix;   // MOD: no row sees a token before `first`, nor one at `prefix` or behind it and its own position
 };
 
-template <int RT, int KT> __device__ __forceinline__ RowTile row_tile(const AttnArgs &p, int m, int len, int j) {
+// Where attn_bounds has left the bounds of row tile j of sequence s, whose first row is r0: a place of its own for each.
+template <int RT> __device__ __forceinline__ int bounds_at(const AttnArgs &p, int s, int r0, int j) { return r0 * p.group.d / RT + s + j; }
+
+template <int RT, int KT, bool MOD> __device__ __forceinline__ RowTile row_tile(const AttnArgs &p, int s, int r0, int m, int len, int j) {
     RowTile t;
     const int first = j * RT;
     t.rows = min(RT, m * p.group.d - first);
     t.pos0 = len - m + p.group.div(first);
     t.pos1 = len - m + p.group.div(first + t.rows - 1);
     const int cap = p.c.table_ld * p.c.page;
+    t.s0 = t.first = t.prefix = 0;
+    if (MOD) {
+        if (p.mod.first || p.mod.prefix) {
+            if (p.c.row_start) {
+                const int2 b = p.mod.bounds[bounds_at<RT>(p, s, r0, j)];
+                t.first = b.x;
+                t.prefix = b.y;
+            } else if (t.pos1 >= 0) {
+                const RowView v = row_view(p, r0, len);
+                t.first = v.first;
+                t.prefix = v.prefix;
+            }
+        }
+        const int low = min(t.first, cap), top = min(max(t.pos1 + 1, t.prefix), cap);
+        const int end = (max(top, 0) + KT - 1) / KT, from = max(low, p.window > 0 ? t.pos0 - p.window + 1 : 0) / KT;
+        t.w0 = min(from, end);
+        t.sinks = 0;
+        if (p.window > 0) {
+            const int keep = max(p.n_sink, t.prefix), stop = min(keep / KT + (keep % KT != 0), t.w0);
+            t.s0 = min(low / KT, stop);
+            t.sinks = stop - t.s0;
+        }
+        t.units = max(1, t.sinks + end - t.w0);
+        return t;
+    }
     const int end = t.pos1 < 0 ? 0 : min(t.pos1, cap - 1) / KT + 1;          // token tiles up to the last row's
     const int from = p.window > 0 ? max(0, t.pos0 - p.window + 1) / KT : 0;   // first tile of the first row's window
     t.w0 = min(from, end);
@@ -80,7 +109,7 @@ struct Cut {
 };
 
 // Where a CTA is in its range.
-template <int RT, int KT, int COST> struct UnitWalk {
+template <int RT, int KT, int COST, bool MOD> struct UnitWalk {
     long long w;             // place of the unit
     int s, h, j, y;          // sequence, kv head, row tile, unit of the row tile
     int r0, m, len, tiles;   // of the sequence: first row, tokens, length, row tiles
@@ -97,7 +126,7 @@ template <int RT, int KT, int COST> struct UnitWalk {
         for (int i = 0; i < tiles; ++i) n += tile_places(p, i);
         return n;
     }
-    __device__ __forceinline__ int tile_places(const AttnArgs &p, int i) const { return row_tile<RT, KT>(p, m, len, i).units + COST; }
+    __device__ __forceinline__ int tile_places(const AttnArgs &p, int i) const { return row_tile<RT, KT, MOD>(p, s, r0, m, len, i).units + COST; }
     // By one warp: the first unit at place `first` or after it, which lies `x` into the
     // sequence, of `per_head` places per kv head.
     __device__ __forceinline__ void start(const AttnArgs &p, long long first, long long x, long long per_head) {
@@ -107,7 +136,7 @@ template <int RT, int KT, int COST> struct UnitWalk {
         if (tiles > kFewTiles) {      // 32 row tiles at a time, one per lane
             const int lane = threadIdx.x & 31;
             for (;; j += 32) {
-                const int n = j + lane < tiles ? row_tile<RT, KT>(p, m, len, j + lane).units + COST : 0;
+                const int n = j + lane < tiles ? row_tile<RT, KT, MOD>(p, s, r0, m, len, j + lane).units + COST : 0;
                 int incl = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -123,10 +152,10 @@ template <int RT, int KT, int COST> struct UnitWalk {
                 }
                 if (j + 32 >= tiles) break;      // not reached: the places end in the sequence
             }
-            t = row_tile<RT, KT>(p, m, len, j);
+            t = row_tile<RT, KT, MOD>(p, s, r0, m, len, j);
         } else {
             for (;; ++j) {
-                t = row_tile<RT, KT>(p, m, len, j);
+                t = row_tile<RT, KT, MOD>(p, s, r0, m, len, j);
                 if (left < t.units + COST) break;
                 left -= t.units + COST;
             }
@@ -134,7 +163,7 @@ template <int RT, int KT, int COST> struct UnitWalk {
         y = max(0, (int)left - COST);
         w = first + y + COST - left;
     }
-    __device__ __forceinline__ int token0() const { return (y < t.sinks ? y : t.w0 + (y - t.sinks)) * KT; }
+    __device__ __forceinline__ int token0() const { return (y < t.sinks ? t.s0 + y : t.w0 + (y - t.sinks)) * KT; }
     // To the first unit of the next item.
     __device__ __forceinline__ void next_item(const AttnArgs &p) {
         w += t.units - y + COST;
@@ -149,7 +178,7 @@ template <int RT, int KT, int COST> struct UnitWalk {
                 } while (m == 0);
             }
         }
-        t = row_tile<RT, KT>(p, m, len, j);
+        t = row_tile<RT, KT, MOD>(p, s, r0, m, len, j);
     }
 };
 
@@ -171,6 +200,8 @@ template <class Walk> __device__ __forceinline__ long long warp_places(const Att
     for (; many; many &= many - 1) {
         const int src = __ffs((int)many) - 1, count = __shfl_sync(0xffffffffu, tiles, src);
         Walk of = walk;
+        of.s = __shfl_sync(0xffffffffu, walk.s, src);
+        of.r0 = __shfl_sync(0xffffffffu, walk.r0, src);
         of.m = __shfl_sync(0xffffffffu, walk.m, src);
         of.len = __shfl_sync(0xffffffffu, walk.len, src);
         long long sum = 0;
@@ -240,7 +271,7 @@ __device__ __forceinline__ Cut find_range(const AttnArgs &p, Walk &walk, long lo
 struct Item {
     int r0, m, len, j, h;      // see UnitWalk
     int y0, n;                 // its units of this CTA: y0 .. y0 + n - 1; n == 0: no more items
-    int rows, pos0, pos1, sinks, w0;
+    int rows, pos0, pos1, s0, sinks, w0, first, prefix;
     int whole;                 // no other CTA has units of it
     int slot;                  // its part's place in the workspace
 };
@@ -256,7 +287,10 @@ template <class Walk> __device__ __forceinline__ Item item_of(const Walk &at, lo
     it.rows = at.t.rows;
     it.pos0 = at.t.pos0;
     it.pos1 = at.t.pos1;
+    it.s0 = at.t.s0;
     it.sinks = at.t.sinks;
+    it.first = at.t.first;
+    it.prefix = at.t.prefix;
     it.w0 = at.t.w0;
     it.n = (int)min((long long)(at.t.units - at.y), last - at.w);
     const long long w0 = at.w - at.y, w1 = w0 + at.t.units - 1;      // places of its first and last unit

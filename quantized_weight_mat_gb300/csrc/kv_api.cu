@@ -111,6 +111,8 @@ KvView view_of(const pq_kv_cache &c, const int *row_start, int n_rows) {
     return v;
 }
 
+size_t bounds_offset(int n_q, int n_kv, int d) { return (pq_attn_ws_bytes(n_q, n_kv, d) + 15) / 16 * 16; }
+
 // pq_attn, and pq_attn_mod where mod asks for something.
 int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt, const void *q, long long ldq, int n_q,
            float scale, int window, int n_sink, const pq_score_mod *mod, void *out, long long ldo, void *ws, size_t ws_bytes,
@@ -165,6 +167,7 @@ int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype 
         a.mod.slope = mod->slope;
         a.mod.first = mod->first;
         a.mod.prefix = mod->prefix;
+        a.mod.bounds = reinterpret_cast<int2 *>(a.ws + bounds_offset(n_q, c.n_kv, c.d));
     }
     const int group = a.group.d;
     const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
@@ -173,7 +176,8 @@ int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype 
     // of 2048 tokens, bf16, head size 128: 16 rows 30.1 us (narrow) against 41.9 (wide), 32 rows 43.3 against 42.4, 64 rows
     // 69.7 against 43.9; head size 64: 28 rows 13.7 against 18.1, 56 rows 18.8 against 18.3. f32 rows keep the pair of fp16
     // for q and for the weights that only the narrow one has.
-    if ((c.d != 64 && c.d != 128) || a.mod.any()) e = launch_attn_generic((int)dt, a, stream);
+    if (c.d != 64 && c.d != 128) e = launch_attn_generic((int)dt, a, stream);
+    else if (a.mod.any()) e = launch_attn_mma_mod((int)dt, a, rows, stream, *dev);
     else if (dt != PQ_F32 && rows > 32) e = launch_attn_tc((int)dt, a, stream, *dev);
     else e = launch_attn_mma((int)dt, a, rows, stream, *dev);
     return e == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
@@ -280,9 +284,9 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
 }
 
 size_t pq_attn_mod_ws_bytes(int n_q, int n_kv, int d, int n_rows, int n_seq) {
-    const size_t plain = pq_attn_ws_bytes(n_q, n_kv, d);
-    if (!plain || n_rows < 0 || n_seq <= 0 || (int64_t)n_rows * n_q > (INT64_C(1) << 30)) return 0;
-    return plain;
+    if (!pq_attn_ws_bytes(n_q, n_kv, d) || n_rows < 0 || n_seq <= 0 || (int64_t)n_rows * n_q > (INT64_C(1) << 30)) return 0;
+    // a place for every row tile of at least 8 rows
+    return bounds_offset(n_q, n_kv, d) + 8 * ((size_t)n_rows * (n_q / n_kv) / 8 + (size_t)n_seq + 1);
 }
 
 int pq_attn_mod(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt, const void *q, long long ldq,

@@ -49,7 +49,7 @@ struct AttnMod {
     float to_unit, top;        // a score times log2 e -> the cap's unit, and the cap times log2 e; 0: no cap
     const float *slope;        // [n_q] or null
     const int *first, *prefix; // [n_rows] or null
-    int2 *bounds;              // of row tiles with several rows: see attn_bounds
+    int2 *bounds;              // of row tiles of several rows: what attn_bounds leaves, behind the workspace of pq_attn
     bool any() const { return top > 0.f || slope || first || prefix; }
 };
 
@@ -73,8 +73,10 @@ cudaError_t launch_kv_gather(int dt, const KvView &c, void *k_out, long long ldk
 // Attention for head sizes 64 and 128, `rows` (tokens times query heads per kv
 // head) of a typical sequence deciding between row tiles of 8 and 16 rows.
 cudaError_t launch_attn_mma(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev);
+cudaError_t launch_attn_mma_mod(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev);
 size_t attn_mma_ws_bytes(int d);
 unsigned attn_mma_wait_timeouts(bool reset);
+unsigned attn_mma_mod_wait_timeouts(bool reset);
 // The same for prompts: 16-bit rows, tensor-core products of 128 rows.
 cudaError_t launch_attn_tc(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev);
 size_t attn_tc_ws_bytes(int d);
