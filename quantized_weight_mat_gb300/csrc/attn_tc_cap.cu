@@ -1,0 +1,21 @@
+// The prompt attention kernel with the capped scores, views and biases of pq_attn_mod.
+
+#include "attn_tc.cuh"
+
+namespace pqk {
+
+unsigned attn_tc_cap_wait_timeouts(bool reset) {
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_wait_timeouts, sizeof(v)) != cudaSuccess) return 0;
+    if (reset) {
+        const unsigned z = 0;
+        cudaMemcpyToSymbol(g_wait_timeouts, &z, sizeof(z));
+    }
+    return v;
+}
+
+cudaError_t launch_attn_tc_cap(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {
+    return a.mod.slope ? launch_dt<kViews | kCap | kBias>(dt, a, s, dev) : launch_dt<kViews | kCap>(dt, a, s, dev);
+}
+
+}  // namespace pqk

@@ -1,0 +1,21 @@
+// The prompt attention kernel with the views and biased scores of pq_attn_mod.
+
+#include "attn_tc.cuh"
+
+namespace pqk {
+
+unsigned attn_tc_mod_wait_timeouts(bool reset) {
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_wait_timeouts, sizeof(v)) != cudaSuccess) return 0;
+    if (reset) {
+        const unsigned z = 0;
+        cudaMemcpyToSymbol(g_wait_timeouts, &z, sizeof(z));
+    }
+    return v;
+}
+
+cudaError_t launch_attn_tc_mod(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {
+    return a.mod.slope ? launch_dt<kViews | kBias>(dt, a, s, dev) : launch_dt<kViews>(dt, a, s, dev);
+}
+
+}  // namespace pqk

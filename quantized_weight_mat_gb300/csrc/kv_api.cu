@@ -176,10 +176,11 @@ int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype 
     // of 2048 tokens, bf16, head size 128: 16 rows 30.1 us (narrow) against 41.9 (wide), 32 rows 43.3 against 42.4, 64 rows
     // 69.7 against 43.9; head size 64: 28 rows 13.7 against 18.1, 56 rows 18.8 against 18.3. f32 rows keep the pair of fp16
     // for q and for the weights that only the narrow one has.
+    const bool wide = dt != PQ_F32 && rows > 32;
     if (c.d != 64 && c.d != 128) e = launch_attn_generic((int)dt, a, stream);
-    else if (a.mod.any()) e = launch_attn_mma_mod((int)dt, a, rows, stream, *dev);
-    else if (dt != PQ_F32 && rows > 32) e = launch_attn_tc((int)dt, a, stream, *dev);
-    else e = launch_attn_mma((int)dt, a, rows, stream, *dev);
+    else if (!a.mod.any()) e = wide ? launch_attn_tc((int)dt, a, stream, *dev) : launch_attn_mma((int)dt, a, rows, stream, *dev);
+    else if (!wide) e = launch_attn_mma_mod((int)dt, a, rows, stream, *dev);
+    else e = a.mod.top > 0.f ? launch_attn_tc_cap((int)dt, a, stream, *dev) : launch_attn_tc_mod((int)dt, a, stream, *dev);
     return e == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
 }
 

@@ -79,8 +79,12 @@ unsigned attn_mma_wait_timeouts(bool reset);
 unsigned attn_mma_mod_wait_timeouts(bool reset);
 // The same for prompts: 16-bit rows, tensor-core products of 128 rows.
 cudaError_t launch_attn_tc(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev);
+cudaError_t launch_attn_tc_mod(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev);      // no cap
+cudaError_t launch_attn_tc_cap(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev);
 size_t attn_tc_ws_bytes(int d);
 unsigned attn_tc_wait_timeouts(bool reset);
+unsigned attn_tc_mod_wait_timeouts(bool reset);
+unsigned attn_tc_cap_wait_timeouts(bool reset);
 // Any head size, CUDA cores.
 cudaError_t launch_attn_generic(int dt, const AttnArgs &a, cudaStream_t s);
 
