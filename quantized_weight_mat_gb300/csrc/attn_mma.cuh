@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     ++k;
                 }
                 if (sub == n) {
-                    tok = at.token0() + 16 * g;
+                    tok = at.token0(MOD && p.mod.slope) + 16 * g;
                     seq = at.s;
                     head = at.h;
                 }
@@ -306,7 +306,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const Item &it = items[k % kItems];
         if (stop || it.n == 0) return;
         const int y0 = it.y0, n = it.n, pos0 = it.pos0, pos1 = it.pos1, sinks = it.sinks, w0 = it.w0;
-        const int s0 = MOD ? it.s0 : 0, lowest = MOD ? it.first : 0, prefix = MOD ? it.prefix : 0;
+        // Scores with a bias by distance rise towards the row's own token: from there back, the references hardly move.
+        const bool back = MOD && p.mod.slope;
+        const int units = MOD ? it.units : 0, s0 = MOD ? it.s0 : 0, lowest = MOD ? it.first : 0, prefix = MOD ? it.prefix : 0;
         if (!dead && !mbar_wait(&q_full, k & 1u)) dead = true;
         {
             if constexpr (NT == 1) {
@@ -339,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         for (int y = y0; y < y0 + n; ++y) {
         if (!dead && !mbar_wait(&full[slot], phase)) dead = true;
-        const int t0 = (y < sinks ? s0 + y : w0 + (y - sinks)) * KT + 32 * warp;
+        const int u = back ? units - 1 - y : y;
+        const int t0 = (u < sinks ? s0 + u : w0 + (u - sinks)) * KT + 32 * warp;
         const TileMeta &mt = meta[slot];
         // both groups: a page, and every row sees every token
         const bool have0 = mt.have[2 * warp], have1 = mt.have[2 * warp + 1];

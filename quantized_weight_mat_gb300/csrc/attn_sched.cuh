@@ -163,7 +163,11 @@ template <int RT, int KT, int COST, bool MOD> struct UnitWalk {
         y = max(0, (int)left - COST);
         w = first + y + COST - left;
     }
-    __device__ __forceinline__ int token0() const { return (y < t.sinks ? t.s0 + y : t.w0 + (y - t.sinks)) * KT; }
+    // First token of the unit; `back`: of the one as far from the item's end.
+    __device__ __forceinline__ int token0(bool back) const {
+        const int u = back ? t.units - 1 - y : y;
+        return (u < t.sinks ? t.s0 + u : t.w0 + (u - t.sinks)) * KT;
+    }
     // To the first unit of the next item.
     __device__ __forceinline__ void next_item(const AttnArgs &p) {
         w += t.units - y + COST;
@@ -271,7 +275,7 @@ __device__ __forceinline__ Cut find_range(const AttnArgs &p, Walk &walk, long lo
 struct Item {
     int r0, m, len, j, h;      // see UnitWalk
     int y0, n;                 // its units of this CTA: y0 .. y0 + n - 1; n == 0: no more items
-    int rows, pos0, pos1, s0, sinks, w0, first, prefix;
+    int rows, pos0, pos1, s0, sinks, w0, units, first, prefix;
     int whole;                 // no other CTA has units of it
     int slot;                  // its part's place in the workspace
 };
@@ -289,6 +293,7 @@ template <class Walk> __device__ __forceinline__ Item item_of(const Walk &at, lo
     it.pos1 = at.t.pos1;
     it.s0 = at.t.s0;
     it.sinks = at.t.sinks;
+    it.units = at.t.units;
     it.first = at.t.first;
     it.prefix = at.t.prefix;
     it.w0 = at.t.w0;

@@ -107,6 +107,23 @@ __device__ __forceinline__ void fma2(uint32_t &x, uint32_t &y, float f, float a)
         : "f"(f), "f"(a));
 }
 
+// (x, y) * (u, v) + a.
+__device__ __forceinline__ void fma2(uint32_t &x, uint32_t &y, float u, float v, float a) {
+    asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n mov.b64 r, {%4, %4};\n"
+        " fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}"
+        : "+r"(x), "+r"(y)
+        : "f"(u), "f"(v), "f"(a));
+}
+__device__ __forceinline__ void fma2(float &x, float &y, float u, float v, float a) {
+    asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n mov.b64 r, {%4, %4};\n"
+        " fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(u), "f"(v), "f"(a));
+}
+// (x, y) squared.
+__device__ __forceinline__ void square2(float &x, float &y) {
+    asm("{\n .reg .b64 p;\n mov.b64 p, {%0, %1};\n mul.rn.f32x2 p, p, p;\n mov.b64 {%0, %1}, p;\n}" : "+f"(x), "+f"(y));
+}
 // (x, y) * f.
 __device__ __forceinline__ void mul2(uint32_t &x, uint32_t &y, float f) {
     asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n mul.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
@@ -245,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++k;
                 }
                 if (sub == n) {
-                    tok = at.token0() + 16 * g;
+                    tok = at.token0((MOD & kBias) != 0) + 16 * g;
                     seq = at.s;
                     head = at.h;
                 }
@@ -367,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t k = 0; !dead; ++k) {
                 if (!mbar_wait(&i_full[k % kItems], (k / kItems) & 1u)) break;
                 const int n = items[k % kItems].n, y0 = items[k % kItems].y0, sinks = items[k % kItems].sinks, w0 = items[k % kItems].w0;
-                const int s0 = MOD ? items[k % kItems].s0 : 0;
+                const int s0 = MOD ? items[k % kItems].s0 : 0, last = (MOD & kBias) ? items[k % kItems].units - 1 : 0;
                 __syncwarp();
                 if (n == 0) break;
                 if (lane == 0) mbar_arrive(&i_empty[k % kItems]);
@@ -401,7 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ts.ve_max = ve_max;
                         ts.have = (int)(haves & 0xffu);
                         ts.plain = (int)(plains & 0xffu);
-                        ts.t0 = (y0 + i < sinks ? s0 + y0 + i : w0 + (y0 + i - sinks)) * KT;
+                        // scores with a bias by distance rise towards the row's own token: from there back, the references hardly move
+                        const int u = (MOD & kBias) ? last - (y0 + i) : y0 + i;
+                        ts.t0 = (u < sinks ? s0 + u : w0 + (u - sinks)) * KT;
                         ts.quick = p.scale >= 0.f && (plains & 0xffu) == 0xffu && lv_min - (float)ve_max > -58.f;
                     }
                     __syncwarp();
@@ -622,35 +641,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     };
                     int done = 0;                             // steps of 32 columns
-                    // weights of the 64 tokens from step done, of those in b0 and b1 if MASK: fp16 pairs times their V scales, the
+                    // weights of the 32 STEPS tokens from step done, of those in b0 and b1 if MASK: fp16 pairs times their V scales, the
                     // sum without the scales, and with them (sw)
-                    uint32_t out[32];
+                    constexpr int STEPS = MOD ? 1 : 2;
+                    uint32_t out[16 * STEPS];
+                    auto store_weights = [&] {      // over columns of S that have been read
+                        if constexpr (STEPS == 2) tmem_st32(ts + 16 * done, out);
+                        else tmem_st16(ts + 16 * done, out);
+                    };
                     float sw;
-                    auto weights = [&](auto mask, uint32_t b0, uint32_t b1) {
-                        constexpr bool MASK = decltype(mask)::value;
+                    // NEAR: scores up to the cap, by a polynomial; `beyond` is then the largest square of a score over the cap
+                    float beyond = 0.f;
+                    auto weights_by = [&](auto mask, auto near_cap, uint32_t b0, uint32_t b1) {
+                        constexpr bool MASK = decltype(mask)::value, NEAR = decltype(near_cap)::value;
                         uint32_t x[2][16];
                         float add = 0.f;
                         sw = 0.f;
                         tmem_ld16(ts + 32 * done, x[0]);
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
+                        for (int g = 0; g < 2 * STEPS; ++g) {
                             float f = sc.ks[2 * done + g] * fac;
                             const float lr = sc.lv[2 * done + g] - (float)vexp, undo = ex2(-lr);
                             float c = have ? lr - m : -INFINITY;
                             const float away = (MOD & kBias) ? (float)(pos - sc.t0 - 32 * done - 16 * g) : 0.f;      // of the group's first token
                             if (MOD & kCap) {
-                                f *= p.mod.to_unit * (2.f * kLog2e);
-                                c += p.mod.top;
+                                f *= NEAR ? p.mod.to_unit : p.mod.to_unit * (2.f * kLog2e);
+                                if (!NEAR) c += p.mod.top;
                             }
                             // where all is seen nothing lies ahead of the row, and the distances fall by 1 a token
                             if ((MOD & kBias) && !MASK) c = fmaf(-slope, away, c);
                             uint32_t(&s)[16] = x[g & 1];
                             tmem_ld_wait(s);
-                            if (g < 3) tmem_ld16(ts + 32 * done + 16 * (g + 1), x[(g + 1) & 1]);
+                            if (g + 1 < 2 * STEPS) tmem_ld16(ts + 32 * done + 16 * (g + 1), x[(g + 1) & 1]);
                             float sx = 0.f, sy = 0.f;
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
-                                if (MOD & kCap) {      // as in capped()
+                                if ((MOD & kCap) && NEAR) {
+                                    mul2(s[e], s[e + 1], f);
+                                    float zx = __uint_as_float(s[e]), zy = __uint_as_float(s[e + 1]);
+                                    square2(zx, zy);
+                                    beyond = fmaxf(fmaxf(beyond, zx), zy);
+                                    float px = p.mod.near[5], py = px;
+#pragma unroll
+                                    for (int k = 4; k >= 0; --k) fma2(px, py, zx, zy, p.mod.near[k]);
+                                    fma2(s[e], s[e + 1], px, py, c);
+                                } else if (MOD & kCap) {      // as in capped()
                                     mul2(s[e], s[e + 1], f);
                                     float ux = ex2(__uint_as_float(s[e])), uy = ex2(__uint_as_float(s[e + 1]));
                                     add2(ux, uy, 1.f, 1.f);
@@ -679,13 +714,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         return add;
                     };
-                    bool go = quick;
+                    auto weights = [&](auto mask, uint32_t b0, uint32_t b1) {
+                        if (MOD & kCap) {
+                            beyond = 0.f;
+                            const float add = weights_by(mask, std::true_type(), b0, b1);
+                            if (!__any_sync(0xffffffffu, beyond > 1.f)) return add;
+                        }
+                        return weights_by(mask, std::false_type(), b0, b1);
+                    };
+                    bool go = quick || (MOD && all);
+                    if constexpr (MOD != 0) {
+#pragma unroll 1
+                        while (go && done < 4) {
+                            const uint32_t b = quick ? ~0u : view(done);
+                            if (!quick && !__any_sync(0xffffffffu, b != 0)) {      // nothing of it is seen
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) out[e] = 0u;
+                                store_weights();
+                                ++done;
+                                continue;
+                            }
+                            const bool whole = quick || __all_sync(0xffffffffu, !have || (b == ~0u && (!(MOD & kBias) || pos - sc.t0 >= 32 * done + 31)));
+                            float add = 0.f;
+                            bool move = !quick && __any_sync(0xffffffffu, b != 0 && m == -INFINITY), moved = false;
+#pragma unroll 1
+                            do {
+                                if (move) {
+                                    raise(done, 1, quick && !have ? 0u : b);
+                                    moved = true;
+                                    go = __all_sync(0xffffffffu, !have || b == 0 || fabsf(m) < kFar);
+                                    if (!go) break;
+                                }
+                                add = whole ? weights(std::false_type(), 0u, 0u) : weights(std::true_type(), b, 0u);
+                                move = !moved && __any_sync(0xffffffffu, have && fmaxf(add, sw) > kMost);      // at the true maximum no weight is above 1
+                            } while (move);
+                            if (!go) break;
+                            l += add;
+                            store_weights();
+                            ++done;
+                        }
+                    } else {
 #pragma unroll 1
                     for (; go && done < 4; done += go ? 2 : 0) {
                         const float add = weights(std::false_type(), 0u, 0u);
                         if (__any_sync(0xffffffffu, have && fmaxf(add, sw) > kMost)) break;      // a reference has to move
                         l += add;
-                        tmem_st32(ts + 16 * done, out);      // over columns of S that have been read
+                        store_weights();
                     }
                     go = all;
 #pragma unroll 1
@@ -706,8 +780,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } while (move);
                         if (!go) break;
                         l += add;
-                        tmem_st32(ts + 16 * done, out);
+                        store_weights();
                         done += 2;
+                    }
                     }
                     // the same with other scales, or far from zero
                     const unsigned plain = near ? (unsigned)sc.plain : 0u;
