@@ -236,7 +236,7 @@ def test_pages_held_beside_the_tables():
     g.compact()
 
 
-@pytest.mark.parametrize("n_pages", [1, 2, 3, 5, 4095, 32768, 32769, 70001, 131075])
+@pytest.mark.parametrize("n_pages", [1, 2, 3, 5, 4095, 16384, 16385, 32769, 70001, 131075])
 def test_pools_of_any_size(n_pages):
     # scanned in one piece and in several, with the ends inside a thread's four
     rng = np.random.default_rng(n_pages)
@@ -257,6 +257,24 @@ def test_pools_of_any_size(n_pages):
         g.compact()
     if n_pages == 1:
         assert g.reserve([1] + [0] * 8) == (0, 0)
+
+
+@pytest.mark.parametrize("n_pages", [16384, 40000])
+def test_requests_of_many_blocks(n_pages):
+    # more blocks than a CTA's threads hold at a time, shared pages among the first and the last of them
+    width = 11000
+    g = make(3, width, n_pages, 16, [16 * 9000 + 5, 0, 7], [(1, 16)])
+    g.fork([0, 2], [1, 2])
+    for t, r in ((g.len, g.ref.len),):              # taken back into pages that both hold
+        t[0] = 3
+        r[0] = 3
+    short, narrow = g.reserve([16 * 9000, 16, 0])
+    assert narrow == 0 and (short > 0) == (n_pages == 16384)
+    g.free([1])
+    assert g.reserve([16 * 9000, 16, 0]) == (0, 0)
+    g.reserve([16 * 20, 16 * 500, 16 * 1000])
+    g.ref.check()
+    g.compact()
 
 
 @pytest.mark.parametrize("n_seq", [1, 255, 256, 1000, 9001])
