@@ -650,7 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else tmem_st16(ts + 16 * done, out);
                     };
                     float sw;
-                    // NEAR: scores up to the cap, by a polynomial; `beyond` is then the largest square of a score over the cap
+                    // NEAR: capped scores of the first three pairs in four by a polynomial, which holds for squares over the cap up
+                    // to kNearCap (`beyond`: the largest), of the fourth as in capped(): the exponentials' unit would take 16
+                    // cycles for each the second way, the multipliers 8 the first way, so both take 7
+                    constexpr float kNearCap = 0.64f;
                     float beyond = 0.f;
                     auto weights_by = [&](auto mask, auto near_cap, uint32_t b0, uint32_t b1) {
                         constexpr bool MASK = decltype(mask)::value, NEAR = decltype(near_cap)::value;
@@ -664,34 +667,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float lr = sc.lv[2 * done + g] - (float)vexp, undo = ex2(-lr);
                             float c = have ? lr - m : -INFINITY;
                             const float away = (MOD & kBias) ? (float)(pos - sc.t0 - 32 * done - 16 * g) : 0.f;      // of the group's first token
-                            if (MOD & kCap) {
-                                f *= NEAR ? p.mod.to_unit : p.mod.to_unit * (2.f * kLog2e);
-                                if (!NEAR) c += p.mod.top;
-                            }
+                            if (MOD & kCap) f *= p.mod.to_unit;
                             // where all is seen nothing lies ahead of the row, and the distances fall by 1 a token
                             if ((MOD & kBias) && !MASK) c = fmaf(-slope, away, c);
+                            const float f2 = f * (2.f * kLog2e), c2 = c + p.mod.top;
                             uint32_t(&s)[16] = x[g & 1];
                             tmem_ld_wait(s);
                             if (g + 1 < 2 * STEPS) tmem_ld16(ts + 32 * done + 16 * (g + 1), x[(g + 1) & 1]);
                             float sx = 0.f, sy = 0.f;
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
-                                if ((MOD & kCap) && NEAR) {
+                                if ((MOD & kCap) && NEAR && e % 8 != 6) {
                                     mul2(s[e], s[e + 1], f);
                                     float zx = __uint_as_float(s[e]), zy = __uint_as_float(s[e + 1]);
                                     square2(zx, zy);
                                     beyond = fmaxf(fmaxf(beyond, zx), zy);
-                                    float px = p.mod.near[5], py = px;
+                                    float px = p.mod.near[4], py = px;
 #pragma unroll
-                                    for (int k = 4; k >= 0; --k) fma2(px, py, zx, zy, p.mod.near[k]);
+                                    for (int k = 3; k >= 0; --k) fma2(px, py, zx, zy, p.mod.near[k]);
                                     fma2(s[e], s[e + 1], px, py, c);
                                 } else if (MOD & kCap) {      // as in capped()
-                                    mul2(s[e], s[e + 1], f);
+                                    mul2(s[e], s[e + 1], f2);
                                     float ux = ex2(__uint_as_float(s[e])), uy = ex2(__uint_as_float(s[e + 1]));
                                     add2(ux, uy, 1.f, 1.f);
                                     s[e] = __float_as_uint(rcp(ux));
                                     s[e + 1] = __float_as_uint(rcp(uy));
-                                    fma2(s[e], s[e + 1], -2.f * p.mod.top, c);
+                                    fma2(s[e], s[e + 1], -2.f * p.mod.top, c2);
                                 } else {
                                     fma2(s[e], s[e + 1], f, c);
                                 }
@@ -714,14 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         return add;
                     };
-                    auto weights = [&](auto mask, uint32_t b0, uint32_t b1) {
-                        if (MOD & kCap) {
-                            beyond = 0.f;
-                            const float add = weights_by(mask, std::true_type(), b0, b1);
-                            if (!__any_sync(0xffffffffu, beyond > 1.f)) return add;
-                        }
-                        return weights_by(mask, std::false_type(), b0, b1);
-                    };
+                    auto weights = [&](auto mask, uint32_t b0, uint32_t b1) { return weights_by(mask, std::false_type(), b0, b1); };
                     bool go = quick || (MOD && all);
                     if constexpr (MOD != 0) {
 #pragma unroll 1
@@ -734,20 +728,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ++done;
                                 continue;
                             }
-                            const bool whole = quick || __all_sync(0xffffffffu, !have || (b == ~0u && (!(MOD & kBias) || pos - sc.t0 >= 32 * done + 31)));
                             float add = 0.f;
-                            bool move = !quick && __any_sync(0xffffffffu, b != 0 && m == -INFINITY), moved = false;
+                            bool fits = quick || __all_sync(0xffffffffu, !have || (b == ~0u && fabsf(m) < kFar && (!(MOD & kBias) || pos - sc.t0 >= 32 * done + 31)));
+                            if (fits) {
+                                beyond = 0.f;
+                                add = weights_by(std::false_type(), std::true_type(), 0u, 0u);
+                                fits = !__any_sync(0xffffffffu, have && (fmaxf(add, sw) > kMost || beyond > kNearCap));
+                            }
+                            if (!fits) {
+                                const uint32_t seen = have ? b : 0u;
+                                bool move = __any_sync(0xffffffffu, seen != 0 && m == -INFINITY), moved = false;
 #pragma unroll 1
-                            do {
-                                if (move) {
-                                    raise(done, 1, quick && !have ? 0u : b);
-                                    moved = true;
-                                    go = __all_sync(0xffffffffu, !have || b == 0 || fabsf(m) < kFar);
-                                    if (!go) break;
-                                }
-                                add = whole ? weights(std::false_type(), 0u, 0u) : weights(std::true_type(), b, 0u);
-                                move = !moved && __any_sync(0xffffffffu, have && fmaxf(add, sw) > kMost);      // at the true maximum no weight is above 1
-                            } while (move);
+                                do {
+                                    if (move) {
+                                        raise(done, 1, seen);
+                                        moved = true;
+                                        go = __all_sync(0xffffffffu, seen == 0 || fabsf(m) < kFar);
+                                        if (!go) break;
+                                    }
+                                    add = weights(std::true_type(), seen, 0u);
+                                    move = !moved && __any_sync(0xffffffffu, fmaxf(add, sw) > kMost);      // at the true maximum no weight is above 1
+                                } while (move);
+                            }
                             if (!go) break;
                             l += add;
                             store_weights();
