@@ -415,24 +415,35 @@ __global__ void __launch_bounds__(kThreads, 2)
             bool all = have0 && have1 && t0 + 31 <= pos0 &&
                        (p.window == 0 || t0 > pos1 - p.window || t0 + 31 < p.n_sink);
             if constexpr (MOD) {
-                bool late = false;                   // some row's first token is behind the tile's
+                if (p.mod.top > 0.f) {
 #pragma unroll
-                for (int x = 0; x < NT; ++x)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = 8 * x + 2 * t + e;
-                        late |= q_view[row].first > t0;
-                        const float slope = q_slope[row], far = (float)(pos[x][e] - t0 - g);
+                        for (int x = 0; x < NT; ++x)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                            for (int e = 0; e < 4; ++e) s[i][x][e] = capped<PAIR>(s[i][x][e], p.mod);
+                }
+                if (p.mod.slope) {
 #pragma unroll
-                            for (int up = 0; up < 2; ++up) {
-                                float &v = s[i][x][e + 2 * up];
-                                if (p.mod.top > 0.f) v = capped<PAIR>(v, p.mod);
-                                v = fmaf(-slope, fabsf(far - (16.f * i + 8.f * up)), v);
-                            }
-                    }
-                all = all && !__any_sync(0xffffffffu, late);
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float slope = q_slope[8 * x + 2 * t + e], far = (float)(pos[x][e] - t0 - g);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int up = 0; up < 2; ++up)
+                                    s[i][x][e + 2 * up] = fmaf(-slope, fabsf(far - (16.f * i + 8.f * up)), s[i][x][e + 2 * up]);
+                        }
+                }
+                if (p.mod.first) {
+                    bool late = false;               // some row's first token is behind the tile's
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) late |= q_view[8 * x + 2 * t + e].first > t0;
+                    all = all && !__any_sync(0xffffffffu, late);
+                }
             }
             uint32_t hidden = 0;                     // bit 4 (2x + i) + e: s[i][x][e] is not seen
             if (!all) {

@@ -71,6 +71,7 @@ constexpr int kImages = 3, kMeta = 4, kItems = 8;
 // An item's rows in and out, its masked tiles and its empty pipeline, in units (2: a prompt of 8192 tokens, 32 heads
 // over 8, 585 us, windowed prompts 94; 6: 470 and 88; 10: 478 and 89).
 constexpr int kItemCost = 6;
+constexpr int kModItemCost = 4;              // with pq_attn_mod's dearer tiles (packed documents: 2: 181 us, 4: 176, 6: 185)
 constexpr int kLeast = 3;                    // places of a CTA (64 rows over 4096 tokens: 8: 32.6 us, 4: 25.0, 3: 24.2, 2: 24.6)
 constexpr int kTcGrid = 160;                 // CTAs at most: one per SM
 constexpr int kTmemCols = 512;
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs p) {
     constexpr uint32_t ID_S = instr_desc(HALF, KT), ID_O = instr_desc(HALF, D) | (1u << 16);      // bit 16: B is MN-major
     constexpr int kRaw = raw_tiles<D>();
-    using Walk = UnitWalk<RT, KT, kItemCost, MOD != 0>;
+    using Walk = UnitWalk<RT, KT, MOD ? kModItemCost : kItemCost, MOD != 0>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], meta_full[kMeta], meta_empty[kMeta], scales_full[kMeta], i_full[kItems],
         i_empty[kItems], image_full[kImages], image_empty[kImages], s_full[2], p_ready[2], pv_done[2], q_ready;
