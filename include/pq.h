@@ -409,7 +409,8 @@ size_t pq_attn_ws_bytes(int n_q, int n_kv, int d);
  * A row at a position below 0 sees nothing.  window and n_sink count from the
  * row's position and the sequence's first token, as in pq_attn.
  *   cap     0, or from 2^-60 to 2^60
- *   slope   device f32 [n_q], or NULL
+ *   slope   device f32 [n_q], or NULL; of any sign (a row is NaN where its is
+ *           not finite)
  *   first, prefix  device int32 [n_rows], or NULL; any values, in any order
  * mod is plain host memory, read during the call only; NULL, or one without
  * any of the four, is pq_attn.  Everything else, the accuracy included, is as in
@@ -485,8 +486,8 @@ int pq_kv_fork(const pq_kv_pool *pool, int n, const int *from, const int *to, co
  * a free one and the codes and scales of the sequence's tokens in it, in all
  * layers (codes behind them stay as they were).  When all who hold a page
  * write to it in this call, the lowest of them keeps it.  Free pages are
- * given out from the lowest number up, in the order of sequences and blocks.
- * len is left to the caller.
+ * given out from the lowest number up, in the order of sequences and blocks; what
+ * they held is still in them.  len is left to the caller.
  *   caches  host array of n_caches handles (up to 1024; may be NULL with 0,
  *           for a pool in which no page with tokens is shared), with the pool's n_pages and
  *           page; their table and len are not looked at

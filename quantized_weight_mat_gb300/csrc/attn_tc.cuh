@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // NEAR: capped scores of the first three pairs in four by a polynomial, which holds for squares over the cap up
                     // to kNearCap (`beyond`: the largest), of the fourth as in capped(): the exponentials' unit would take 16
                     // cycles for each the second way, the multipliers 8 the first way, so both take 7
-                    constexpr float kNearCap = 0.64f;
+                    constexpr float kNearCap = 0.64f, kLargest = 3.4e38f;
                     float beyond = 0.f;
                     auto weights_by = [&](auto mask, auto near_cap, uint32_t b0, uint32_t b1) {
                         constexpr bool MASK = decltype(mask)::value, NEAR = decltype(near_cap)::value;
@@ -668,10 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float lr = sc.lv[2 * done + g] - (float)vexp, undo = ex2(-lr);
                             float c = have ? lr - m : -INFINITY;
                             const float away = (MOD & kBias) ? (float)(pos - sc.t0 - 32 * done - 16 * g) : 0.f;      // of the group's first token
-                            if (MOD & kCap) f *= p.mod.to_unit;
+                            if (MOD & kCap) f = fminf(f * p.mod.to_unit, kLargest);      // a score of 0 stays 0
                             // where all is seen nothing lies ahead of the row, and the distances fall by 1 a token
                             if ((MOD & kBias) && !MASK) c = fmaf(-slope, away, c);
-                            const float f2 = f * (2.f * kLog2e), c2 = c + p.mod.top;
+                            const float f2 = fminf(f * (2.f * kLog2e), kLargest), c2 = c + p.mod.top;
                             uint32_t(&s)[16] = x[g & 1];
                             tmem_ld_wait(s);
                             if (g + 1 < 2 * STEPS) tmem_ld16(ts + 32 * done + 16 * (g + 1), x[(g + 1) & 1]);

@@ -194,6 +194,67 @@ def test_hidden_pages_may_hold_nan(dt, news, ws):  # noqa: F811
     run(c, news, dt, 4, ws, first=first, slope=modref.slopes(4), window=90, sinks=70)
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 2, 64)])
+@pytest.mark.parametrize("news", [None, [40], [300]])
+@pytest.mark.parametrize("what", ["cap", "bias"])
+def test_scales_of_very_different_pages(dt, heads, news, what, ws):  # noqa: F811
+    # pages of key scales from tiny to so large that their scores are all far beyond the cap, zero keys among them
+    n_q, n_kv, d = heads
+    c = kvref.Cache(1, [700], n_kv, 32, d, seed=14)
+    rng = np.random.default_rng(14)
+    named = c.table[0]
+    c.vs[named] *= 10.0 ** rng.integers(-6, 3, (len(named), n_kv))
+    if what == "cap":
+        c.ks[named[::3]] *= 1e12
+        c.ks[named[1::5]] *= 1e-9
+        c.k[named[::6]] = 0
+        run(c, news, dt, n_q, ws, cap=3.0)
+        run(c, news, dt, n_q, ws, cap=2.0 ** -60)
+    else:
+        run(c, news, dt, n_q, ws, slope=modref.slopes(n_q))
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("rows", [1, 40])
+def test_long_contexts(dt, rows, ws):  # noqa: F811
+    # one row tile shared by many CTAs, from the row's own token back; documents that begin far into the sequence
+    n = 20000
+    c = kvref.Cache(1, [n], 2, 64, 64, seed=15)
+    news = None if rows == 1 else [rows]
+    run(c, news, dt, 8, ws, slope=modref.slopes(8) / 16)
+    run(c, news, dt, 8, ws, cap=20.0, first=np.full(rows, 9000, np.int32), prefix=np.full(rows, 9100, np.int32), window=3000)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_two_streams_with_a_workspace_each(dt):
+    import torch
+    c = kvref.Cache(3, [900, 400, 150], 2, 32, 128, seed=16)
+    _, h = upload(c)
+    rs = torch.tensor([0, 300, 500, 510], dtype=torch.int32, device="cuda")
+    slope = torch.from_numpy(modref.slopes(8)).cuda()
+    first = torch.full((510,), 50, dtype=torch.int32, device="cuda")
+    mods = [pq.pq_score_mod(20.0, None, first), pq.pq_score_mod(0.0, slope)]
+    qs = [torch.randn(510, 1024, device="cuda").to(tdt(dt)) for _ in mods]
+    size = pq.pq_attn_mod_ws_bytes(8, 2, 128, 510, 3)
+    wss = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in mods]
+
+    def call(i, out, stream=None):
+        pq.pq_attn_mod(h, rs, 510, dt, qs[i], 1024, 8, 0.1, 0, 0, mods[i], out, 1024, wss[i], size, stream=stream)
+
+    want = [torch.empty_like(q) for q in qs]
+    for i in (0, 1):
+        call(i, want[i])
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in mods], [[torch.empty_like(q) for _ in range(20)] for q in qs]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i in (0, 1):
+            call(i, outs[i][k], streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in (0, 1) for o in outs[i])
+
+
 @pytest.mark.parametrize("news", [None, [257, 1]])
 def test_in_a_cuda_graph_with_bounds_that_move(news, ws):  # noqa: F811
     import torch

@@ -318,6 +318,45 @@ def test_steps_in_a_graph():
     g.ref.check()
 
 
+def test_give_back_and_compact_in_a_graph():
+    import torch
+    g = make(6, 12, 80, 16, [100, 150, 60, 0, 90, 10], [(2, 64)] * 2, room=20)
+    g.fork([0], [3], [33])
+    seq, begin, end = ints([1, 3, 5]), ints([0, 0, 0]), ints([0, 0, 0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pq.pq_kv_free(g.pool, 3, seq, begin, end)
+        pq.pq_kv_compact(g.pool, g.layers, g.moved, g.status[2:], g.ws, g.n_ws)
+    for b, e in (([20, 0, 3], [150, 16, 3]), ([0, 17, 0], [16, 40, 10]), ([0, 0, 0], [1000, 1000, 1000])):
+        begin.copy_(ints(b))
+        end.copy_(ints(e))
+        graph.replay()
+        g.ref.free([1, 3, 5], b, e)
+        moved, used = g.ref.compact()
+        assert int(g.status[2]) == used and np.array_equal(g.moved.cpu().numpy(), np.append(moved, -9))
+        g.check()
+    g.ref.check()
+
+
+def test_lists_of_views_and_layers_apart():
+    # lists that are slices of others, layers that lie in no order
+    import torch
+    r = poolref.Pool(5, 6, 40, 16, [(2, 32), (1, 64), (2, 32)], 3)
+    r.fill([50, 20, 0, 0, 33], 3)
+    g = Gpu(r)
+    order = [2, 0, 1]
+    layers = pq.pq_kv_layers([g.layers[i] for i in order])
+    both = ints([7, 0, 4, 2, 3, 9])
+    g.ref.fork([0, 4], [2, 3])
+    pq.pq_kv_fork(g.pool, 2, both[1:], both[3:], None, g.ws, g.n_ws)
+    new = ints([5, 1, 0, 0, 1, 1, 5])
+    assert g.ref.reserve([1, 0, 0, 1, 1]) == (0, 0)
+    pq.pq_kv_reserve(g.pool, layers, new[1:], g.status, g.ws, g.n_ws)
+    torch.cuda.synchronize()
+    g.check()
+
+
 def test_two_pools_on_two_streams():
     import torch
     gs = [make(5, 8, 60, 32, [100, 0, 0, 200, 0], seed=s) for s in (1, 2)]
