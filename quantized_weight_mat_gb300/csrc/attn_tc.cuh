@@ -92,6 +92,12 @@ template <int D> __device__ __forceinline__ uint32_t image_at(int row, int chunk
     return (uint32_t)(row >> 3) * (16 * D) + chunk * 128 + (row & 7) * 16;
 }
 
+// 16 bytes (or zeros when !have) to shared memory, asynchronously and past the L1 cache; and the wait for a thread's own.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ float lg2(float x) {
@@ -487,19 +493,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (act) {
                 // the row of q: power-of-two scale, fp16, operand image
                 const T *mine = static_cast<const T *>(p.q) + (it.r0 + tok) * p.ldq + (long long)head * D;
-                // 8 rows by 64 bytes a load: whole sectors of global memory, and no two lanes on one bank of the image
+                // through the rows' own part of the operand image, whole rows a load and no two lanes on one bank either way: loads to
+                // registers, 8 rows by 64 bytes each for the sake of the banks, took 4200 cycles to issue
                 constexpr int PER = D / 32;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int src = i * ROWS + sub;
+                    const unsigned long long row = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), src);
+                    copy16(stage + src * D * 2 + ((ch ^ (src & 7)) << 4), reinterpret_cast<const uint4 *>(row) + ch, row0 + src < it.rows);
+                }
+                copies_wait();
+                __syncwarp();
                 uint4 w[4][PER];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int src = 8 * i + (lane & 7);
-                    const uint4 *row = reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), src));
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        w[i][j] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row0 + src < it.rows) w[i][j] = row[4 * j + (lane >> 3)];
-                    }
-                }
+                    for (int j = 0; j < PER; ++j)
+                        w[i][j] = lds128(stage + (8 * i + (lane & 7)) * D * 2 + (((4 * j + (lane >> 3)) ^ (lane & 7)) << 4));
+                __syncwarp();
                 uint32_t top[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
