@@ -34,6 +34,10 @@
 // 54, of 4096 (f32) 12.0, of which 4.5 pass before the first tile is there (lengths,
 // table, TMA) and 2.5 in the second kernel.  More warps of 16 tokens each: 78 us against 64.
 //
+// pq_attn_mod (MOD) changes scores and views between the two products: one row over 4096 tokens, capped, 13.2 us (12.2
+// without), 64 ragged sequences biased by distance 72 (67), windowed steps capped 49 (47): the loop waits on latency, and the loads hide
+// only part of the instructions.
+//
 // Pipeline: warp 4 walks the CTA's units (the other warps get each item from it
 // through a small ring) and brings 128-token tiles of K and V through a ring of
 // stages (one TMA box per page, swizzled; page numbers read for four tiles at a
