@@ -1,6 +1,7 @@
 // The decode-step attention kernel with the scores and views of pq_attn_mod.
 
-#include "attn_mma.cuh"
+#define PQ_ATTN_MOD
+#include "attn_mma.cu"
 
 namespace pqk {
 

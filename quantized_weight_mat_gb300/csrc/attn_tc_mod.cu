@@ -1,6 +1,7 @@
 // The prompt attention kernel with the views and biased scores of pq_attn_mod.
 
-#include "attn_tc.cuh"
+#define PQ_ATTN_MOD
+#include "attn_tc.cu"
 
 namespace pqk {
 
