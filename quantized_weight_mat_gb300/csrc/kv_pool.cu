@@ -289,6 +289,7 @@ template <int RANKS> __global__ void __cluster_dims__(RANKS, 1, 1) __launch_boun
     a.n = min(per, p.n_seq - a.s0);
     int *count = w.list[1], *lowest = w.list[2], turn = 0;      // count: writers of a page less its holders; lowest: the lowest sequence that writes
     unsigned sum;
+    if (RANKS > 1) sync_all<RANKS>();      // all CTAs run: their boards may be written
     wait_for_inputs();
     if (tid == 0) w.head[0] = 0;
 
@@ -444,6 +445,7 @@ template <int RANKS> __global__ void __cluster_dims__(RANKS, 1, 1) __launch_boun
     __shared__ unsigned sums[kPlanWarps];
     const int tid = blockIdx.x * kPlanThreads + threadIdx.x;
     int *holes = w.list[0], *live = w.list[1], *map = w.list[2], turn = 0;
+    if (RANKS > 1) sync_all<RANKS>();      // all CTAs run: their boards may be written
     wait_for_inputs();
     unsigned sum, n = 0, used = 0;
     for (int i0 = 0; i0 < p.n_pages; i0 += sweep<RANKS>()) {
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) move_pages(const __gr
         const uint4 *src = reinterpret_cast<const uint4 *>(codes) + from * row;
         uint4 *dst = reinterpret_cast<uint4 *>(codes) + to * row;
         // Unit f is number f - u * units of head u: the quotient by a reciprocal, which is off by less than the half that
-        // keeps it from the next whole number (u below 2^6, units at most 2^11).
+        // keeps it from the next whole number (u below 2^5, units at most 2^11).
         const float inv = 1.f / (float)units;
         constexpr int AT_ONCE = 4;
         for (int f0 = lane; f0 < total; f0 += 32 * AT_ONCE) {
