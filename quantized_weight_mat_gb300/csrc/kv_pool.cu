@@ -257,7 +257,7 @@ template <int N> __device__ __forceinline__ void look(const PoolView &p, const A
     int held[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        const int at = i + e * kPlanThreads, s = at < items ? seq_of(a, at) : 0;
+        const int at = i + e * kPlanThreads, s = at >= items ? 0 : at < kCached ? a.seen[at].y : seq_of(a, at);
         x[e] = make_int2(-1, s);
         if (at < items) x[e].x = row_of(p, a.s0 + s)[a.first[s] + at - a.start[s]];
     }
@@ -317,7 +317,10 @@ template <int RANKS> __global__ void __cluster_dims__(RANKS, 1, 1) __launch_boun
     if (threadIdx.x == 0) a.start[a.n] = items;
     __syncthreads();
 
-    // which of them lack a page, and which have one that others hold too
+    // their sequences, a warp each; then which of them lack a page, and which have one that others hold too
+    for (int s = threadIdx.x >> 5; s < a.n; s += kPlanWarps)
+        for (int i = a.start[s] + lane; i < min(a.start[s + 1], kCached); i += 32) a.seen[i].y = s;
+    __syncthreads();
     bool any = false;
     constexpr int N = 4;
     for (int i = threadIdx.x; i < items; i += N * kPlanThreads) {
