@@ -20,8 +20,8 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // x = score * log2 e -> cap * tanh(score / cap) * log2 e, from tanh y = 1 - 2 / (1 + e^2y): the exponential's and the
-// quotient's errors are absolute ones, cap * 2^-21 of the score, which 16-bit rows do not see. EXACT: a relative one, by
-// the Taylor series below y = 0.4 (its next term is 2^-24 of the sum there).
+// quotient's errors are absolute ones, cap * 2^-21 of the score, which 16-bit rows do not see. EXACT: a relative one,
+// 2^-20, by the Taylor series below y = 0.4 (its next term is 2^-24 of the sum there).
 template <bool EXACT> __device__ __forceinline__ float capped(float x, const AttnMod &m) {
     const float y = x * m.to_unit;
     const float far = fmaf(rcp(1.f + ex2(y * (2.f * kLog2e))), -2.f * m.top, m.top);
