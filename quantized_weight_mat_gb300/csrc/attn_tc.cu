@@ -631,16 +631,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         float a = 1.f;
+                        bool turn = false;      // whether something is stored in the old units: not of a row that saw nothing before
                         if (top > -INFINITY) {
                             const float mn = fmaxf(m, ceilf(top));
                             const int up = m == -INFINITY ? kFarExp : (int)fminf(mn - m, (float)kFarExp);
                             // O's unit 2^(m + vexp) stays while m moves, as far as vexp can follow
                             const int vn = max(max(vexp - up, kLeastExp), (int)ceilf(fmaxf(tv + (top - mn), -(float)kFarExp)));
                             a = pow2(vexp - up - vn);
+                            turn = m > -INFINITY && a != 1.f;
                             l *= pow2(-up);
                             m = mn;
                             vexp = vn;
                         }
+                        if (!__any_sync(0xffffffffu, turn)) return;
                         rescale(a);
 #pragma unroll 1
                         for (int i = 0; i < c; ++i) {
