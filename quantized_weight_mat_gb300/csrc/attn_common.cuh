@@ -176,17 +176,20 @@ template <class T, int D, int RT> __global__ void __launch_bounds__(256) attn_jo
     }
 }
 
-// What the rows of each row tile see at most: the first token of any, and the end of any's prefix (pq_attn_mod calls of
-// several rows per sequence, whose row tiles are counted by every CTA). A warp per row tile; sequences in blockIdx.x.
-constexpr int kBoundsWarps = 8, kBoundsSplit = 8;
-template <int RT> __global__ void __launch_bounds__(32 * kBoundsWarps) attn_bounds(AttnArgs p) {
+// What the rows of each row tile see at most, the first token of any and the end of any's prefix, and the places of a kv head
+// of each sequence (pq_attn_mod calls of several rows per sequence: else every CTA would look them up for all row tiles
+// before its first unit). A warp per row tile; sequences in blockIdx.x, every kBoundsSplit * kBoundsWarps row tiles in blockIdx.y.
+constexpr int kBoundsWarps = 8;
+template <int RT, int COST> __global__ void __launch_bounds__(32 * kBoundsWarps) attn_bounds(AttnArgs p) {
+    __shared__ long long sums[kBoundsWarps];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int lane = threadIdx.x & 31, s = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.x;
     int r0, m;
     seq_rows(p.c, s, r0, m);
     const int len = seq_len(p.c, s), rows = m * p.group.d;
-    for (int j = blockIdx.y * kBoundsWarps + (threadIdx.x >> 5); j * RT < rows; j += kBoundsSplit * kBoundsWarps) {
+    long long places = 0;
+    for (int j = blockIdx.y * kBoundsWarps + warp; j * RT < rows; j += kBoundsSplit * kBoundsWarps) {
         const int end = p.group.div(min((j + 1) * RT, rows) - 1);
         int first = INT_MAX, prefix = 0;
         for (int tok = p.group.div(j * RT) + lane; tok <= end; tok += 32)
@@ -197,10 +200,19 @@ template <int RT> __global__ void __launch_bounds__(32 * kBoundsWarps) attn_boun
             }
         first = __reduce_min_sync(0xffffffffu, first);
         prefix = __reduce_max_sync(0xffffffffu, prefix);
-        if (lane == 0) p.mod.bounds[bounds_at<RT>(p, s, r0, j)] = make_int2(first, prefix);
+        if (lane == 0) {
+            p.mod.bounds[bounds_at<RT>(p, s, r0, j)] = make_int2(first, prefix);
+            places += row_tile<RT, KT, true>(p, s, r0, m, len, j).units + COST;
+        }
+    }
+    if (lane == 0) sums[warp] = places;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kBoundsWarps; ++i) places += sums[i];
+        p.mod.places[(size_t)s * kBoundsSplit + blockIdx.y] = places;
     }
 }
-template <int RT> cudaError_t launch_bounds(const AttnArgs &a, cudaStream_t s) {
+template <int RT, int COST> cudaError_t launch_bounds(const AttnArgs &a, cudaStream_t s) {
     if (!a.c.row_start || !(a.mod.first || a.mod.prefix)) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.c.n_seq, kBoundsSplit);
@@ -211,7 +223,7 @@ template <int RT> cudaError_t launch_bounds(const AttnArgs &a, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_bounds<RT>, a);
+    return cudaLaunchKernelEx(&cfg, attn_bounds<RT, COST>, a);
 }
 
 // Launches an attention kernel and the join of its parts, each so that it may be

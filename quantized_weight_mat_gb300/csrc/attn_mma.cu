@@ -712,7 +712,7 @@ template <class T, int D, int NT, bool MOD> cudaError_t launch(const AttnArgs &a
     long long grid = 2 * dev.sm_count;
     if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
     if (row_tiles < grid && tiles * row_tiles * a.c.n_kv < grid) grid = tiles * row_tiles * a.c.n_kv;
-    if (MOD && (e = launch_bounds<8 * NT>(a, s)) != cudaSuccess) return e;
+    if (MOD && (e = launch_bounds<8 * NT, kItemCost>(a, s)) != cudaSuccess) return e;
     return launch_with_join<T, D, 8 * NT>(attn_mma<T, D, NT, MOD>, (int)grid, kThreads, smem, km, vm, a, s);
 }
 

@@ -110,6 +110,7 @@ struct Cut {
 
 // Where a CTA is in its range.
 template <int RT, int KT, int COST, bool MOD> struct UnitWalk {
+    static constexpr bool kMod = MOD;
     long long w;             // place of the unit
     int s, h, j, y;          // sequence, kv head, row tile, unit of the row tile
     int r0, m, len, tiles;   // of the sequence: first row, tokens, length, row tiles
@@ -186,12 +187,24 @@ template <int RT, int KT, int COST, bool MOD> struct UnitWalk {
     }
 };
 
+// Whether attn_bounds has run for the call.
+__device__ __forceinline__ bool counted(const AttnArgs &p) { return p.c.row_start && (p.mod.first || p.mod.prefix); }
+
 // Places of the whole call, by one warp; lane 0's `walk` of every group of 32
 // sequences is not kept.
 template <class Walk> __device__ __forceinline__ long long warp_places(const AttnArgs &p, int s, Walk &walk, int lane) {
     walk.s = s + lane;
     walk.m = 0;
     if (walk.s < p.c.n_seq) walk.seq(p);
+    if (Walk::kMod && counted(p)) {
+        long long n = 0;
+        if (walk.m > 0) {
+            const longlong2 *of = reinterpret_cast<const longlong2 *>(p.mod.places + (size_t)walk.s * kBoundsSplit);
+#pragma unroll
+            for (int i = 0; i < kBoundsSplit / 2; ++i) n += of[i].x + of[i].y;
+        }
+        return n;
+    }
     const int tiles = walk.m > 0 ? walk.tiles : 0;
     // a few sequences of many row tiles one after the other, by all lanes: about 4 row tiles' time each, and one more
     // per 32 of them

@@ -947,7 +947,7 @@ template <class T, int D, int MOD> cudaError_t launch(const AttnArgs &a, cudaStr
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
     if (!make_map(&km, a.c.k, a.c) || !make_map(&vm, a.c.v, a.c)) return cudaErrorInvalidValue;
-    if (MOD && (e = launch_bounds<RT>(a, s)) != cudaSuccess) return e;
+    if (MOD && (e = launch_bounds<RT, kModItemCost>(a, s)) != cudaSuccess) return e;
     return launch_with_join<T, D, RT>(attn_tc<T, D, MOD>, dev.sm_count < kTcGrid ? dev.sm_count : kTcGrid, kThreads, smem, km, vm, a, s);
 }
 

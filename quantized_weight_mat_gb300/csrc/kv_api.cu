@@ -170,7 +170,8 @@ int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype 
         a.mod.slope = mod->slope;
         a.mod.first = mod->first;
         a.mod.prefix = mod->prefix;
-        a.mod.bounds = reinterpret_cast<int2 *>(a.ws + bounds_offset(n_q, c.n_kv, c.d));
+        a.mod.places = reinterpret_cast<long long *>(a.ws + bounds_offset(n_q, c.n_kv, c.d));
+        a.mod.bounds = reinterpret_cast<int2 *>(a.mod.places + (size_t)c.n_seq * kBoundsSplit);
     }
     const int group = a.group.d;
     const int rows = row_start ? (int)(((int64_t)n_rows + c.n_seq - 1) / c.n_seq) * group : group;
@@ -289,8 +290,8 @@ int pq_attn(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype
 
 size_t pq_attn_mod_ws_bytes(int n_q, int n_kv, int d, int n_rows, int n_seq) {
     if (!pq_attn_ws_bytes(n_q, n_kv, d) || n_rows < 0 || n_seq <= 0 || (int64_t)n_rows * n_q > (INT64_C(1) << 30)) return 0;
-    // a place for every row tile of at least 8 rows
-    return bounds_offset(n_q, n_kv, d) + 8 * ((size_t)n_rows * (n_q / n_kv) / 8 + (size_t)n_seq + 1);
+    // numbers for every sequence, and a place for every row tile of at least 8 rows
+    return bounds_offset(n_q, n_kv, d) + 8 * ((size_t)n_rows * (n_q / n_kv) / 8 + (kBoundsSplit + 1) * (size_t)n_seq + 1);
 }
 
 int pq_attn_mod(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype dt, const void *q, long long ldq,

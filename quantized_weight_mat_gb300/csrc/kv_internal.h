@@ -44,13 +44,17 @@ struct KvAppendArgs {
     FastDiv units, per_row;      // d / 16, and n_q times that
 };
 
+constexpr int kBoundsSplit = 8;
 // What pq_attn_mod does to scores and views; all empty in pq_attn.
 struct AttnMod {
     float to_unit, top;        // a score times log2 e -> the cap's unit, and the cap times log2 e; 0: no cap
     float near[5];             // of the polynomial that stands for the cap's curve up to 0.8 caps, times `top`
     const float *slope;        // [n_q] or null
     const int *first, *prefix; // [n_rows] or null
-    int2 *bounds;              // of row tiles of several rows: what attn_bounds leaves, behind the workspace of pq_attn
+    // of sequences of several rows, what attn_bounds leaves behind the workspace of pq_attn: their row tiles' bounds, and the
+    // places of one kv head (see attn_sched.cuh) in kBoundsSplit parts
+    int2 *bounds;
+    long long *places;
     bool any() const { return top > 0.f || slope || first || prefix; }
 };
 
