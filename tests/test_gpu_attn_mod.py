@@ -255,6 +255,41 @@ def test_two_streams_with_a_workspace_each(dt):
     assert all(torch.equal(o, want[i]) for i in (0, 1) for o in outs[i])
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 2, 64), (4, 2, 80)])
+@pytest.mark.parametrize("news", [None, [40], [300]])
+@pytest.mark.parametrize("what", ["ks", "vs", "q"])
+def test_nan_reaches_the_rows_that_see_it(dt, heads, news, what, ws):  # noqa: F811
+    # a NaN behind the cap and beside the bias: all of the rows that see it, none of the others
+    import torch
+    n_q, n_kv, d = heads
+    c = kvref.Cache(1, [700], n_kv, 32, d, seed=17)
+    n = 1 if news is None else news[0]
+    pos = np.arange(700 - n, 700)
+    if what != "q":
+        getattr(c, what)[c.table[0, 20], 1] = np.nan       # tokens 640 to 671 of the second kv head
+    first = np.where(np.arange(n) % 3 == 0, 672, 0).astype(np.int32)
+    first = np.minimum(first, pos).astype(np.int32)
+    _, h = upload(c)
+    q = torch.randn(n, n_q * d, device="cuda").to(tdt(dt))
+    if what == "q":
+        q[n // 2, 5] = float("nan")                        # the first query head of one row
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    rs = None if news is None else torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for mod in (pq.pq_score_mod(5.0, None, dev(first)), pq.pq_score_mod(0.0, dev(modref.slopes(n_q)), dev(first)),
+                pq.pq_score_mod(5.0, dev(modref.slopes(n_q)), dev(first))):
+        out = torch.zeros_like(q)
+        pq.pq_attn_mod(h, rs, n, dt, q, n_q * d, n_q, d ** -0.5, 0, 0, mod, out, n_q * d, ws, ws.numel())
+        torch.cuda.synchronize()
+        nan = out.float().cpu().isnan().view(n, n_q, d).numpy()
+        want = np.zeros((n, n_q, d), bool)
+        if what == "q":
+            want[n // 2, 0] = True
+        else:
+            want[(first < 672) & (pos >= 640), n_q // n_kv:] = True
+        assert np.array_equal(nan, want)
+
+
 @pytest.mark.parametrize("news", [None, [257, 1]])
 def test_in_a_cuda_graph_with_bounds_that_move(news, ws):  # noqa: F811
     import torch

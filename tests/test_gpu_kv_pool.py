@@ -357,6 +357,40 @@ def test_lists_of_views_and_layers_apart():
     g.check()
 
 
+def test_offsets_past_32_bits():
+    import torch
+    n_kv, page, d = 8, 64, 128
+    n_pages = 2 ** 32 // (n_kv * page * d) + 64
+    k = torch.zeros(n_pages, n_kv, page, d, dtype=torch.int8, device="cuda")
+    v = torch.zeros_like(k)
+    ks, vs = torch.zeros(n_pages, n_kv, device="cuda"), torch.zeros(n_pages, n_kv, device="cuda")
+    top = n_pages - 3
+    for x in (k, v):
+        x[top] = torch.randint(-127, 128, (n_kv, page, d), dtype=torch.int8, device="cuda")
+    ks[top], vs[top] = 1.5, 2.5
+    was = [x[top].clone() for x in (k, v, ks, vs)]
+    # all pages but the last two are in use, the one before them by two sequences
+    refs = torch.ones(n_pages, dtype=torch.int32, device="cuda")
+    refs[top], refs[top + 1:] = 2, 0
+    table = torch.tensor([[top, -1], [top, -1]], dtype=torch.int32, device="cuda")
+    ln = torch.tensor([40, 40], dtype=torch.int32, device="cuda")
+    pool = pq.pq_kv_pool(refs, table, ln, n_pages, page, 2, 2)
+    layers = pq.pq_kv_layers([pq.pq_kv_cache(k, v, ks, vs, table, ln, n_pages, n_kv, page, d, 2, 2)])
+    ws = torch.empty(pq.pq_kv_pool_ws_bytes(pool), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(3, dtype=torch.int32, device="cuda")
+    pq.pq_kv_reserve(pool, layers, ints([0, 1]), status, ws, ws.numel())
+    assert status.tolist() == [0, 0, 0] and table.tolist() == [[top, -1], [top + 1, -1]]
+    for x, y in zip((k, v), was):
+        assert torch.equal(x[top + 1, :, :40], y[:, :40]) and not x[top + 1, :, 40:].any()
+    assert torch.equal(ks[top + 1], was[2]) and torch.equal(vs[top + 1], was[3])
+    # the others are given back, and both move to the bottom
+    refs[:top] = 0
+    pq.pq_kv_compact(pool, layers, None, status[2:], ws, ws.numel())
+    assert status.tolist() == [0, 0, 2] and table.tolist() == [[0, -1], [1, -1]]
+    assert all(torch.equal(x[0], y) for x, y in zip((k, v, ks, vs), was))
+    assert refs[:2].tolist() == [1, 1] and not refs[2:].any()
+
+
 def test_two_pools_on_two_streams():
     import torch
     gs = [make(5, 8, 60, 32, [100, 0, 0, 200, 0], seed=s) for s in (1, 2)]
