@@ -11,6 +11,7 @@
 namespace pqk {
 namespace {
 
+enum : int { kViews = 1, kCap = 2, kBias = 4 };     // of pq_attn_mod: first tokens and prefixes (with the others too), capped, biased scores
 constexpr int KT = 128;                      // tokens per tile
 constexpr int kGroups = KT / 16;             // groups of 16 tokens: always within one page
 constexpr int kMinExp = -200, kMaxExp = 125;   // of V scales: one that takes no part, and the largest

@@ -98,8 +98,8 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// MOD: scores and views of pq_attn_mod.
-template <class T, int D, int NT, bool MOD>
+// MOD: 0 for pq_attn, else kViews and what else of pq_attn_mod.
+template <class T, int D, int NT, int MOD>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_mma(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs p) {
     constexpr int RT = 8 * NT, NS = stages<D>(), CH = D / 16;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int kLift = 7;                         // weights are at most 2^kSlack R: this far up, fp16 holds them and as many small ones as it can
     constexpr int RLD = red_pitch<D>(), QP = q_pitch<D>();
     constexpr int AHEAD_C = NT == 1 ? CH / 2 : 1;    // K chunk pairs loaded ahead of their use
-    using Walk = UnitWalk<RT, KT, kItemCost, MOD>;
+    using Walk = UnitWalk<RT, KT, kItemCost, MOD != 0>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], i_full[kItems], i_empty[kItems], q_full, q_empty;
     __shared__ __align__(16) TileMeta meta[NS];
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ float red_m[kConsumers][RT], red_l[kConsumers][RT], q_fac[RT];
     __shared__ int q_pos[RT];
     __shared__ RowView q_view[MOD ? RT : 1];
-    __shared__ float q_slope[MOD ? RT : 1];
+    __shared__ float q_slope[(MOD & kBias) ? RT : 1];
     __shared__ volatile int stop;
 
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -194,9 +194,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     q_fac[r] = down * (p.scale * kLog2e);
                     q_pos[r] = r < it.rows ? it.len - it.m + tok[i] : -1;
                     q_out[r] = (it.r0 + tok[i]) * p.ldo + (long long)head[i] * D;
-                    if constexpr (MOD) {
+                    if constexpr (MOD != 0) {
                         q_view[r] = q_pos[r] >= 0 ? row_view(p, it.r0 + tok[i], it.len) : RowView{0, 0};
-                        q_slope[r] = p.mod.slope && r < it.rows ? p.mod.slope[head[i]] * kLog2e : 0.f;
+                        if constexpr ((MOD & kBias) != 0) q_slope[r] = r < it.rows ? p.mod.slope[head[i]] * kLog2e : 0.f;
                     }
                 }
             }
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     ++k;
                 }
                 if (sub == n) {
-                    tok = at.token0(MOD && p.mod.slope) + 16 * g;
+                    tok = at.token0((MOD & kBias) != 0) + 16 * g;
                     seq = at.s;
                     head = at.h;
                 }
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (stop || it.n == 0) return;
         const int y0 = it.y0, n = it.n, pos0 = it.pos0, pos1 = it.pos1, sinks = it.sinks, w0 = it.w0;
         // Scores with a bias by distance rise towards the row's own token: from there back, the references hardly move.
-        const bool back = MOD && p.mod.slope;
-        const int units = MOD ? it.units : 0, s0 = MOD ? it.s0 : 0, lowest = MOD ? it.first : 0, prefix = MOD ? it.prefix : 0;
+        constexpr bool back = (MOD & kBias) != 0;
+        const int units = back ? it.units : 0, s0 = MOD ? it.s0 : 0, lowest = MOD ? it.first : 0, prefix = MOD ? it.prefix : 0;
         if (!dead && !mbar_wait(&q_full, k & 1u)) dead = true;
         {
             if constexpr (NT == 1) {
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int e = 0; e < 4; ++e) s[i][x][e] = (s[i][x][e] + s2[i][x][e]) * (ks[i] * fac[x][e & 1]);
             bool all = have0 && have1 && t0 + 31 <= pos0 &&
                        (p.window == 0 || t0 > pos1 - p.window || t0 + 31 < p.n_sink);
-            if constexpr (MOD) {
-                if (p.mod.top > 0.f) {
+            if constexpr (MOD != 0) {
+                if constexpr ((MOD & kCap) != 0) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) s[i][x][e] = capped<PAIR>(s[i][x][e], p.mod);
                 }
-                if (p.mod.slope) {
+                if constexpr ((MOD & kBias) != 0) {
 #pragma unroll
                     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-template <class T, int D, int NT, bool MOD> cudaError_t launch(const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {
+template <class T, int D, int NT, int MOD> cudaError_t launch(const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {
     constexpr int smem = smem_bytes<D, NT, sizeof(T) == 4>();
     static PerDeviceOnce once;
     cudaError_t e = once.run([] {
@@ -716,14 +716,14 @@ template <class T, int D, int NT, bool MOD> cudaError_t launch(const AttnArgs &a
     return launch_with_join<T, D, 8 * NT>(attn_mma<T, D, NT, MOD>, (int)grid, kThreads, smem, km, vm, a, s);
 }
 
-template <class T, bool MOD> cudaError_t launch_t(const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
+template <class T, int MOD> cudaError_t launch_t(const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
     // Rows on the narrow side of a product: 8, or 16 where a sequence brings more than 8 per kv head (16 rows, 64
     // sequences of 2048 tokens, 32 heads over 8: 70.5 us, as two times 8 rows 92.7; 16 sequences 30.2 and 29.1).
     if (a.c.d == 128) return rows <= 8 ? launch<T, 128, 1, MOD>(a, s, dev) : launch<T, 128, 2, MOD>(a, s, dev);
     return rows <= 8 ? launch<T, 64, 1, MOD>(a, s, dev) : launch<T, 64, 2, MOD>(a, s, dev);
 }
 
-template <bool MOD> cudaError_t launch_dt(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
+template <int MOD> cudaError_t launch_dt(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
     if (dt == PQ_F32) return launch_t<float, MOD>(a, rows, s, dev);
     if (dt == PQ_F16) return launch_t<__half, MOD>(a, rows, s, dev);
     return launch_t<__nv_bfloat16, MOD>(a, rows, s, dev);
@@ -746,7 +746,7 @@ unsigned attn_mma_wait_timeouts(bool reset) {
 size_t attn_mma_ws_bytes(int d) { return attn_splits_bytes() + 2 * kAttnMaxGrid * attn_part_floats(16, d) * 4; }
 
 cudaError_t launch_attn_mma(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
-    return launch_dt<false>(dt, a, rows, s, dev);
+    return launch_dt<0>(dt, a, rows, s, dev);
 }
 
 #endif

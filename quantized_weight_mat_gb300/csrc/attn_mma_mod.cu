@@ -1,4 +1,4 @@
-// The decode-step attention kernel with the scores and views of pq_attn_mod.
+// The decode-step attention kernel with the views and biased scores of pq_attn_mod.
 
 #define PQ_ATTN_MOD
 #include "attn_mma.cu"
@@ -16,7 +16,7 @@ unsigned attn_mma_mod_wait_timeouts(bool reset) {
 }
 
 cudaError_t launch_attn_mma_mod(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
-    return launch_dt<true>(dt, a, rows, s, dev);
+    return a.mod.slope ? launch_dt<kViews | kBias>(dt, a, rows, s, dev) : launch_dt<kViews>(dt, a, rows, s, dev);
 }
 
 }  // namespace pqk

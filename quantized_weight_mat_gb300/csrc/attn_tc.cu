@@ -80,7 +80,6 @@ constexpr int kTcGrid = 160;                 // CTAs at most: one per SM
 constexpr int kTmemCols = 512;
 constexpr float kMost = 32768.f;             // the running maximum moves when a row's weights of one step sum to more: fp16 holds each
 constexpr float kFar = 1048576.f;            // maxima up to here leave room for the V scales beside them
-enum : int { kViews = 1, kCap = 2, kBias = 4 };     // of pq_attn_mod: first tokens and prefixes (with the others too), capped, biased scores
 
 // raw tiles, K and V in turn
 template <int D> __host__ __device__ constexpr int raw_tiles() { return D == 128 ? 4 : 8; }

@@ -183,8 +183,8 @@ int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype 
     const bool wide = dt != PQ_F32 && rows > 32;
     if (c.d != 64 && c.d != 128) e = launch_attn_generic((int)dt, a, stream);
     else if (!a.mod.any()) e = wide ? launch_attn_tc((int)dt, a, stream, *dev) : launch_attn_mma((int)dt, a, rows, stream, *dev);
-    else if (!wide) e = launch_attn_mma_mod((int)dt, a, rows, stream, *dev);
-    else e = a.mod.top > 0.f ? launch_attn_tc_cap((int)dt, a, stream, *dev) : launch_attn_tc_mod((int)dt, a, stream, *dev);
+    else if (a.mod.top > 0.f) e = wide ? launch_attn_tc_cap((int)dt, a, stream, *dev) : launch_attn_mma_cap((int)dt, a, rows, stream, *dev);
+    else e = wide ? launch_attn_tc_mod((int)dt, a, stream, *dev) : launch_attn_mma_mod((int)dt, a, rows, stream, *dev);
     return e == cudaSuccess ? PQ_OK : PQ_ERR_LAUNCH;
 }
 

@@ -78,10 +78,12 @@ cudaError_t launch_kv_gather(int dt, const KvView &c, void *k_out, long long ldk
 // Attention for head sizes 64 and 128, `rows` (tokens times query heads per kv
 // head) of a typical sequence deciding between row tiles of 8 and 16 rows.
 cudaError_t launch_attn_mma(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev);
-cudaError_t launch_attn_mma_mod(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev);
+cudaError_t launch_attn_mma_mod(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev);      // no cap
+cudaError_t launch_attn_mma_cap(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev);
 size_t attn_mma_ws_bytes(int d);
 unsigned attn_mma_wait_timeouts(bool reset);
 unsigned attn_mma_mod_wait_timeouts(bool reset);
+unsigned attn_mma_cap_wait_timeouts(bool reset);
 // The same for prompts: 16-bit rows, tensor-core products of 128 rows.
 cudaError_t launch_attn_tc(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev);
 cudaError_t launch_attn_tc_mod(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev);      // no cap

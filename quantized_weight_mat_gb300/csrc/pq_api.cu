@@ -344,7 +344,7 @@ int pq_wait_timeouts(int reset) {
     if (check_device(&dev)) return PQ_ERR_DEVICE;
     const unsigned n =
         stream_wait_timeouts(reset != 0) + tc_wait_timeouts(reset != 0) + selftest_wait_timeouts(reset != 0) +
-        attn_mma_wait_timeouts(reset != 0) + attn_mma_mod_wait_timeouts(reset != 0) + attn_tc_wait_timeouts(reset != 0) +
+        attn_mma_wait_timeouts(reset != 0) + attn_mma_mod_wait_timeouts(reset != 0) + attn_mma_cap_wait_timeouts(reset != 0) + attn_tc_wait_timeouts(reset != 0) +
         attn_tc_mod_wait_timeouts(reset != 0) + attn_tc_cap_wait_timeouts(reset != 0);
     return n > 0x7fffffffu ? 0x7fffffff : (int)n;
 }
