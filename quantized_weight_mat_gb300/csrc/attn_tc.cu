@@ -589,12 +589,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_st_wait();
                     };
-                    // a score times log2 e, of the tile's token e, capped and biased
-                    auto modified = [&](float x, int e) {
+                    // a score times log2 e of a token `away` before the row's own, capped and biased; of the tile's token e
+                    auto modified = [&](float x, float away) {
                         if (MOD & kCap) x = capped<false>(x, p.mod);
-                        if (MOD & kBias) x = fmaf(-slope, fabsf((float)(pos - sc.t0 - e)), x);
+                        if (MOD & kBias) x = fmaf(-slope, fabsf(away), x);
                         return x;
                     };
+                    auto before = [&](int e) { return (MOD & kBias) ? (float)(pos - sc.t0 - e) : 0.f; };
                     // ---- mostly all rows see the whole tile. V scales in the exponent: at most 2^60 below the reference, which
                     // may move to ve_max, and beside a maximum whose last bit does not swallow them
                     bool near = true, all = true;
@@ -618,11 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t x[16];
                             tmem_ld16(ts + 16 * g, x);
                             tmem_ld_wait(x);
-                            const float f = sc.ks[g] * fac;
+                            const float f = sc.ks[g] * fac, away = before(16 * g);
                             float most = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                if ((bits >> e) & 1) most = fmaxf(most, modified(__fmul_rn(__uint_as_float(x[e]), f), 16 * g + e));
+                                if ((bits >> e) & 1) most = fmaxf(most, modified(__fmul_rn(__uint_as_float(x[e]), f), away - (float)e));
                             if (most > -INFINITY) {
                                 const float t = fmaxf(top, most);
                                 tv = fmaxf(tv + (top - t), (float)sc.ve[g] + (most - t));
@@ -683,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float f = sc.ks[2 * done + g] * fac;
                             const float lr = sc.lv[2 * done + g] - (float)vexp, undo = ex2(-lr);
                             float c = have ? lr - m : -INFINITY;
-                            const float away = (MOD & kBias) ? (float)(pos - sc.t0 - 32 * done - 16 * g) : 0.f;      // of the group's first token
+                            const float away = before(32 * done + 16 * g);      // of the group's first token
                             if (MOD & kCap) f = fminf(f * p.mod.to_unit, kLargest);      // a score of 0 stays 0
                             // where all is seen nothing lies ahead of the row, and the distances fall by 1 a token
                             if ((MOD & kBias) && !MASK) c = fmaf(-slope, away, c);
@@ -826,12 +827,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int gi = 0; gi < 2; ++gi) {
                                 const int g = 2 * done + gi;
                                 const bool in = (plain >> g) & 1;      // the V scale is in the exponent
-                                const float f = sc.ks[g] * fac, lr = in ? sc.lv[g] - (float)vexp : 0.f;
+                                const float f = sc.ks[g] * fac, lr = in ? sc.lv[g] - (float)vexp : 0.f, away = before(16 * g);
                                 float w[16], sx = 0.f, sy = 0.f;
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
                                     const bool see = (bits >> (16 * gi + e)) & 1;
-                                    w[e] = ex2(see ? modified(__fmul_rn(__uint_as_float(x[16 * gi + e]), f), 16 * g + e) - base + lr : -INFINITY);
+                                    w[e] = ex2(see ? modified(__fmul_rn(__uint_as_float(x[16 * gi + e]), f), away - (float)e) - base + lr : -INFINITY);
                                 }
 #pragma unroll
                                 for (int e = 0; e < 16; e += 2) add2(sx, sy, w[e], w[e + 1]);
