@@ -52,7 +52,7 @@
 // pq_attn_mod (MOD): 32 columns at a time, so that code fetch keeps up (a cap over 64: 573 us where 32 took 470), those that
 // nobody sees passed over, biased items from the row's own token back. Capped scores cost 14 cycles a pair in the
 // multipliers and 14 in the exponentials' unit, see kNearCap: the same 2048 rows 433 us; two halves' weights, which run side by
-// side, take 3500 cycles of a tile's 6400. Packed documents (2 x 4096 rows, about 700 tokens each) 167 us, a third of it the starts
+// side, take 3500 cycles of a tile's 6400. Packed documents (2 x 4096 rows, about 700 tokens each) 169 us, a third of it the starts
 // and ends of items of 4 tiles.
 // Tiles at an edge of some row's view take the same step with a mask; tiles
 // with missing pages, with scales that are no ordinary positive numbers, or
