@@ -11,7 +11,9 @@
 namespace pqk {
 namespace {
 
-enum : int { kViews = 1, kCap = 2, kBias = 4 };     // of pq_attn_mod: first tokens and prefixes (with the others too), capped, biased scores
+// Of pq_attn_mod: first tokens and prefixes (with the others too), capped, biased scores; kExact: caps that 16-bit rows need
+// relative errors for, biased or not.
+enum : int { kViews = 1, kCap = 2, kBias = 4, kExact = 8 | kViews | kCap | kBias };
 constexpr int KT = 128;                      // tokens per tile
 constexpr int kGroups = KT / 16;             // groups of 16 tokens: always within one page
 constexpr int kMinExp = -200, kMaxExp = 125;   // of V scales: one that takes no part, and the largest
@@ -175,6 +177,11 @@ template <class T, int D, int RT> __global__ void __launch_bounds__(256) attn_jo
         store4(static_cast<T *>(p.out) + (it.r0 + tk) * p.ldo + (long long)hd * D + 4 * col,
                make_float4(acc[r].x * inv, acc[r].y * inv, acc[r].z * inv, acc[r].w * inv));
     }
+}
+
+// The slope of a query head in log2 units.
+template <int MOD> __device__ __forceinline__ float slope_of(const AttnArgs &p, int head) {
+    return MOD == kExact && !p.mod.slope ? 0.f : p.mod.slope[head] * kLog2e;
 }
 
 // What the rows of each row tile see at most, the first token of any and the end of any's prefix, and the places of a kv head

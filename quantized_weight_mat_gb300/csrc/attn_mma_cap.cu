@@ -16,6 +16,8 @@ unsigned attn_mma_cap_wait_timeouts(bool reset) {
 }
 
 cudaError_t launch_attn_mma_cap(int dt, const AttnArgs &a, int rows, cudaStream_t s, const DeviceInfo &dev) {
+    if (a.mod.large && dt == PQ_F16) return launch_t<__half, kExact>(a, rows, s, dev);
+    if (a.mod.large && dt == PQ_BF16) return launch_t<__nv_bfloat16, kExact>(a, rows, s, dev);
     return a.mod.slope ? launch_dt<kViews | kCap | kBias>(dt, a, rows, s, dev) : launch_dt<kViews | kCap>(dt, a, rows, s, dev);
 }
 

@@ -20,7 +20,8 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // x = score * log2 e -> cap * tanh(score / cap) * log2 e, from tanh y = 1 - 2 / (1 + e^2y): the exponential's and the
-// quotient's errors are absolute ones, cap * 2^-21 of the score, which 16-bit rows do not see. EXACT: a relative one, 2^-22,
+// quotient's errors are absolute ones, cap * 2^-21 of the score, which 16-bit rows do not see up to caps of 256 (at 10^6 it
+// is 0.1 and more). EXACT, for f32 rows and larger caps: a relative one, 2^-22,
 // below y = 0.8 by y + y^3 Q(y^2), Q fitted there for the least largest error (2^-23.9; 2^-22.8 evaluated in f32); from
 // there on the first form is as good. (The Taylor series to 0.4 instead: one f32 row over 4096 tokens up to 1.1e-6 off.)
 template <bool EXACT> __device__ __forceinline__ float capped(float x, const AttnMod &m) {

@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs p) {
     constexpr uint32_t ID_S = instr_desc(HALF, KT), ID_O = instr_desc(HALF, D) | (1u << 16);      // bit 16: B is MN-major
     constexpr int kRaw = raw_tiles<D>();
+    constexpr bool EXACT = MOD == kExact;
     using Walk = UnitWalk<RT, KT, MOD ? kModItemCost : kItemCost, MOD != 0>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], meta_full[kMeta], meta_empty[kMeta], scales_full[kMeta], i_full[kItems],
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             RowView row_sees = {0, 0};
             float slope = 0.f;
             if (MOD && pos >= 0) row_sees = row_view(p, it.r0 + tok, it.len);
-            if ((MOD & kBias) && have) slope = p.mod.slope[head] * kLog2e;
+            if ((MOD & kBias) && have) slope = slope_of<MOD>(p, head);
             if (act) {
                 // the row of q: power-of-two scale, fp16, operand image
                 const T *mine = static_cast<const T *>(p.q) + (it.r0 + tok) * p.ldq + (long long)head * D;
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     // a score times log2 e of a token `away` before the row's own, capped and biased; of the tile's token e
                     auto modified = [&](float x, float away) {
-                        if (MOD & kCap) x = capped<false>(x, p.mod);
+                        if (MOD & kCap) x = capped<EXACT>(x, p.mod);
                         if (MOD & kBias) x = fmaf(-slope, fabsf(away), x);
                         return x;
                     };
@@ -671,10 +672,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // NEAR: capped scores of the first three pairs in four by a polynomial, which holds for squares over the cap up
                     // to kNearCap (`beyond`: the largest), of the fourth as in capped(): the exponentials' unit would take 16
                     // cycles for each the second way, the multipliers 8 the first way, so both take 7
-                    constexpr float kNearCap = 0.64f, kLargest = 3.4e38f;
+                    // EXACT: all by the polynomial, and where that does not hold by capped<true>() in the last of the loops below (2048
+                    // rows over 10240 tokens 520 us, all by the last loop 1479)
+                    constexpr float kNearCap = EXACT ? 0.36f : 0.64f, kLargest = 3.4e38f;
                     float beyond = 0.f;
                     auto weights_by = [&](auto mask, auto near_cap, uint32_t b0, uint32_t b1) {
-                        constexpr bool MASK = decltype(mask)::value, NEAR = decltype(near_cap)::value;
+                        constexpr bool MASK = decltype(mask)::value, NEAR = EXACT || decltype(near_cap)::value;
                         uint32_t x[2][16];
                         float add = 0.f;
                         sw = 0.f;
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float sx = 0.f, sy = 0.f;
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
-                                if ((MOD & kCap) && NEAR && e % 8 != 6) {
+                                if ((MOD & kCap) && NEAR && (EXACT || e % 8 != 6)) {
                                     mul2(s[e], s[e + 1], f);
                                     float zx = __uint_as_float(s[e]), zy = __uint_as_float(s[e + 1]);
                                     square2(zx, zy);
@@ -752,6 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 beyond = 0.f;
                                 add = weights_by(std::false_type(), std::true_type(), 0u, 0u);
                                 fits = !__any_sync(0xffffffffu, have && (fmaxf(add, sw) > kMost || beyond > kNearCap));
+                                go = !EXACT || !__any_sync(0xffffffffu, have && beyond > kNearCap);
+                                if (!go) break;
                             }
                             if (!fits) {
                                 const uint32_t seen = have ? b : 0u;
@@ -764,7 +769,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         go = __all_sync(0xffffffffu, seen == 0 || fabsf(m) < kFar);
                                         if (!go) break;
                                     }
+                                    beyond = 0.f;
                                     add = weights(std::true_type(), seen, 0u);
+                                    go = !EXACT || !__any_sync(0xffffffffu, seen != 0 && beyond > kNearCap);
+                                    if (!go) break;
                                     move = !moved && __any_sync(0xffffffffu, fmaxf(add, sw) > kMost);      // at the true maximum no weight is above 1
                                 } while (move);
                             }

@@ -16,6 +16,7 @@ unsigned attn_tc_cap_wait_timeouts(bool reset) {
 }
 
 cudaError_t launch_attn_tc_cap(int dt, const AttnArgs &a, cudaStream_t s, const DeviceInfo &dev) {
+    if (a.mod.large) return launch_dt<kExact>(dt, a, s, dev);
     return a.mod.slope ? launch_dt<kViews | kCap | kBias>(dt, a, s, dev) : launch_dt<kViews | kCap>(dt, a, s, dev);
 }
 

@@ -163,9 +163,13 @@ int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype 
         if (mod->cap > 0.f) {
             a.mod.top = (float)(mod->cap * 1.4426950408889634);
             a.mod.to_unit = (float)(1 / (mod->cap * 1.4426950408889634));
-            // tanh(y) = y P(y^2) for |y| <= 0.8, P fitted there for the least largest error (2^-21.5; 2^-21.2 evaluated in f32)
-            const double near[5] = {0.999995135, -0.333174266, 0.131862197, -0.0482613155, 0.0114646552};
-            for (int i = 0; i < 5; ++i) a.mod.near[i] = (float)(near[i] * mod->cap * 1.4426950408889634);
+            // up to 256 an error of 2^-21 of the cap moves a 16-bit output by less than its rounding
+            a.mod.large = mod->cap > 256.f;
+            // tanh(y) = y P(y^2) for |y| <= 0.8, P fitted there for the least largest error (2^-21.5; 2^-21.2 evaluated in
+            // f32); for large caps to 0.6 with P(0) = 1, for the least relative one (2^-23.5; 2^-22.9)
+            const double wide[5] = {0.999995135, -0.333174266, 0.131862197, -0.0482613155, 0.0114646552};
+            const double tight[5] = {1, -0.333325975, 0.133131167, -0.0522118076, 0.0156126341};
+            for (int i = 0; i < 5; ++i) a.mod.near[i] = (float)((a.mod.large ? tight : wide)[i] * mod->cap * 1.4426950408889634);
         }
         a.mod.slope = mod->slope;
         a.mod.first = mod->first;
