@@ -1,6 +1,7 @@
 // Scores and views of pq_attn_mod: the cap, the bias by distance, a row's first token and prefix.
 #pragma once
 
+#include "attn_cap.cuh"
 #include "kv_device.cuh"
 
 namespace pqk {
@@ -19,22 +20,8 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// x = score * log2 e -> cap * tanh(score / cap) * log2 e, from tanh y = 1 - 2 / (1 + e^2y): the exponential's and the
-// quotient's errors are absolute ones, cap * 2^-21 of the score, which 16-bit rows do not see up to caps of 256 (at 10^6 it
-// is 0.1 and more). EXACT, for f32 rows and larger caps: a relative one, 2^-22,
-// below y = 0.8 by y + y^3 Q(y^2), Q fitted there for the least largest error (2^-23.9; 2^-22.8 evaluated in f32); from
-// there on the first form is as good. (The Taylor series to 0.4 instead: one f32 row over 4096 tokens up to 1.1e-6 off.)
 template <bool EXACT> __device__ __forceinline__ float capped(float x, const AttnMod &m) {
-    const float y = x * m.to_unit;
-    const float far = fmaf(rcp(1.f + ex2(y * (2.f * kLog2e))), -2.f * m.top, m.top);
-    if (!EXACT) return far;
-    const float z = y * y;
-    float s = fmaf(z, -0.00441088624f, 0.0191907637f);
-    s = fmaf(z, s, -0.0531763146f);
-    s = fmaf(z, s, 0.133227658f);
-    s = fmaf(z, s, -0.33332867f);
-    s = fmaf(z * y, s, y) * m.top;
-    return fabsf(y) < 0.8f ? s : far;
+    return cap_score<EXACT>(x, m.to_unit, m.top, [](float v) { return ex2(v); }, [](float v) { return rcp(v); });
 }
 
 // What a row sees beside what its position says: tokens from `first` on, and all below `prefix` (kept below len).

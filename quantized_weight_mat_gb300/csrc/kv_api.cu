@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "attn_cap.cuh"
 #include "kv_checks.h"
 
 using namespace pqk;
@@ -161,9 +162,8 @@ int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype 
     a.mod = AttnMod{};
     if (mod) {
         if (mod->cap > 0.f) {
-            a.mod.top = (float)(mod->cap * 1.4426950408889634);
-            a.mod.to_unit = (float)(1 / (mod->cap * 1.4426950408889634));
-            // up to 256 an error of 2^-21 of the cap moves a 16-bit output by less than its rounding
+            cap_constants(mod->cap, a.mod.top, a.mod.to_unit);
+            // up to 256 an error of 2^-20 of the cap moves a 16-bit output by about its rounding at most
             a.mod.large = mod->cap > 256.f;
             // tanh(y) = y P(y^2) for |y| <= 0.8, P fitted there for the least largest error (2^-21.5; 2^-21.2 evaluated in
             // f32); for large caps to 0.6 with P(0) = 1, for the least relative one (2^-23.5; 2^-22.9)

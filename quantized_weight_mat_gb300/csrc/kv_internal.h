@@ -48,7 +48,7 @@ constexpr int kBoundsSplit = 8;
 // What pq_attn_mod does to scores and views; all empty in pq_attn.
 struct AttnMod {
     float to_unit, top;        // a score times log2 e -> the cap's unit, and the cap times log2 e; 0: no cap
-    bool large;                // a cap of which 16-bit rows would see 2^-21
+    bool large;                // a cap of which 16-bit rows would see 2^-20
     float near[5];             // of the polynomial that stands for the cap's curve up to 0.8 caps (large: 0.6), times `top`
     const float *slope;        // [n_q] or null
     const int *first, *prefix; // [n_rows] or null
