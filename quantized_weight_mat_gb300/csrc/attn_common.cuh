@@ -179,11 +179,6 @@ template <class T, int D, int RT> __global__ void __launch_bounds__(256) attn_jo
     }
 }
 
-// The slope of a query head in log2 units.
-template <int MOD> __device__ __forceinline__ float slope_of(const AttnArgs &p, int head) {
-    return MOD == kExact && !p.mod.slope ? 0.f : p.mod.slope[head] * kLog2e;
-}
-
 // What the rows of each row tile see at most, the first token of any and the end of any's prefix, and the places of a kv head
 // of each sequence (pq_attn_mod calls of several rows per sequence: else every CTA would look them up for all row tiles
 // before its first unit). A warp per row tile; sequences in blockIdx.x, every kBoundsSplit * kBoundsWarps row tiles in blockIdx.y.

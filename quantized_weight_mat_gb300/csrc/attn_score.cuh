@@ -24,6 +24,14 @@ template <bool EXACT> __device__ __forceinline__ float capped(float x, const Att
     return cap_score<EXACT>(x, m.to_unit, m.top, [](float v) { return ex2(v); }, [](float v) { return rcp(v); });
 }
 
+// The slope of a query head in log2 units, 0 without one. An infinite one is NaN, so that every score that a row sees is: of
+// tokens all ahead of a row the prompt kernel would otherwise take none, and give zeros.
+__device__ __forceinline__ float slope_of(const AttnArgs &p, int head) {
+    if (!p.mod.slope) return 0.f;
+    const float s = p.mod.slope[head];
+    return fabsf(s) < INFINITY ? s * kLog2e : __int_as_float(0x7fc00000);
+}
+
 // What a row sees beside what its position says: tokens from `first` on, and all below `prefix` (kept below len).
 struct RowView {
     int first, prefix;

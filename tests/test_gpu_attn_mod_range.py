@@ -1,4 +1,4 @@
-"""pq_attn_mod at the ends of what it takes: caps far above the scores.
+"""pq_attn_mod at the ends of what it takes: caps far above the scores, slopes that are no numbers.
 
 Bounds as in test_gpu_attn.py: 4e-5 for the scores (times `wide`, how much larger than usual they are), 2^-11 for the weights
 of 16-bit rows, the output's own rounding.  The cap's error is 2^-21 of a capped score (below 16 * wide times log2 e), or
@@ -89,6 +89,25 @@ def test_large_caps_beside_biases_and_views(dt, heads, news, ws):  # noqa: F811
     check(*attend(c, news, dt, n_q, ws, cap=1e6, slope=modref.slopes(n_q)), dt, off=off + bias)
     first = np.random.default_rng(23).integers(0, 650, n).astype(np.int32)
     check(*attend(c, news, dt, n_q, ws, cap=1e6, first=first, prefix=np.full(n, 640, np.int32), window=90, sinks=20), dt, off=off)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("news", NEWS)
+def test_a_slope_that_is_no_number_spoils_its_own_head(dt, heads, news, ws):  # noqa: F811
+    n_q, n_kv, d = heads
+    c = kvref.Cache(1, [700], n_kv, 32, d, seed=25)
+    slope = np.array([1.0, np.inf, np.nan, -np.inf, 0.25, 0.0, -0.01, 0.5], np.float32)[:n_q]
+    sane = np.where(np.isfinite(slope), slope, 0.0).astype(np.float32)
+    n = 1 if news is None else news[0]
+    for views in ({}, dict(first=(np.arange(700 - n, 700) + 2).astype(np.int32), prefix=np.full(n, 700, np.int32))):
+        got, _, _ = attend(c, news, dt, n_q, ws, slope=slope, **views)
+        _, ref, vmax = attend(c, news, dt, n_q, ws, slope=sane, **views)
+        sees = vmax > 0
+        bad = ~np.isfinite(slope)
+        assert np.isnan(got[:, bad][sees[:, bad]]).all()
+        assert (got[~sees] == 0).all()
+        check(got[:, ~bad], ref[:, ~bad], vmax[:, ~bad], dt, off=3 * 2.0 ** -24 * LOG2E * (64 + 7))
 
 
 def test_no_wait_ran_out():
