@@ -409,8 +409,8 @@ size_t pq_attn_ws_bytes(int n_q, int n_kv, int d);
  * A row at a position below 0 sees nothing.  window and n_sink count from the
  * row's position and the sequence's first token, as in pq_attn.
  *   cap     0, or from 2^-60 to 2^60
- *   slope   device f32 [n_q], or NULL; of any sign (a row that sees something
- *           is NaN where its is not finite)
+ *   slope   device f32 [n_q], or NULL; of any sign, magnitudes above 2^96 count
+ *           as 2^96 (a row that sees something is NaN where its is not finite)
  *   first, prefix  device int32 [n_rows], or NULL; any values, in any order
  * mod is plain host memory, read during the call only; NULL, or one without
  * any of the four, is pq_attn.  Everything else, the accuracy included, is as in

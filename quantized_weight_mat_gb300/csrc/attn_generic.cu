@@ -43,7 +43,7 @@ template <class T, bool MOD> __global__ void __launch_bounds__(32 * kWarps) attn
     float slope = 0.f;
     if (MOD) {
         if (pos >= 0) view = row_view(p, r, seq_len(c, s));
-        slope = slope_of(p, h);
+        slope = slope_of<true>(p, h);
     }
     const int end = (int)min((long long)max(pos + 1, view.prefix), (long long)c.table_ld * c.page);
     const int from = p.window > 0 ? max(0, pos - p.window + 1) : 0;      // first token of the window

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     q_out[r] = (it.r0 + tok[i]) * p.ldo + (long long)head[i] * D;
                     if constexpr (MOD != 0) {
                         q_view[r] = q_pos[r] >= 0 ? row_view(p, it.r0 + tok[i], it.len) : RowView{0, 0};
-                        if constexpr ((MOD & kBias) != 0) q_slope[r] = r < it.rows ? slope_of(p, head[i]) : 0.f;
+                        if constexpr ((MOD & kBias) != 0) q_slope[r] = r < it.rows ? slope_of<MOD == kExact>(p, head[i]) : 0.f;
                     }
                 }
             }

@@ -24,12 +24,14 @@ template <bool EXACT> __device__ __forceinline__ float capped(float x, const Att
     return cap_score<EXACT>(x, m.to_unit, m.top, [](float v) { return ex2(v); }, [](float v) { return rcp(v); });
 }
 
-// The slope of a query head in log2 units, 0 without one. An infinite one is NaN, so that every score that a row sees is: of
-// tokens all ahead of a row the prompt kernel would otherwise take none, and give zeros.
-__device__ __forceinline__ float slope_of(const AttnArgs &p, int head) {
-    if (!p.mod.slope) return 0.f;
+// The slope of a query head in log2 units; MAYBE: 0 if there are none. An infinite one is NaN, so that every score that a row sees is: of
+// tokens all ahead of a row the prompt kernel would otherwise take none, and give zeros. A finite one counts up to 2^96: times
+// the largest distance (below 2^31) and log2 e it stays below 2^128, where a bias of -infinity would make NaN of warps that
+// see no nearer token; between tokens at different distances nothing but the nearer one counts either way.
+template <bool MAYBE> __device__ __forceinline__ float slope_of(const AttnArgs &p, int head) {
+    if (MAYBE && !p.mod.slope) return 0.f;
     const float s = p.mod.slope[head];
-    return fabsf(s) < INFINITY ? s * kLog2e : __int_as_float(0x7fc00000);
+    return fmaf(fminf(fmaxf(s, -0x1p96f), 0x1p96f), kLog2e, s - s);      // s - s: 0, or NaN
 }
 
 // What a row sees beside what its position says: tokens from `first` on, and all below `prefix` (kept below len).

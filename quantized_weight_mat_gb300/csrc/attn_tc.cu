@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             RowView row_sees = {0, 0};
             float slope = 0.f;
             if (MOD && pos >= 0) row_sees = row_view(p, it.r0 + tok, it.len);
-            if ((MOD & kBias) && have) slope = slope_of(p, head);
+            if ((MOD & kBias) && have) slope = slope_of<MOD == kExact>(p, head);
             if (act) {
                 // the row of q: power-of-two scale, fp16, operand image
                 const T *mine = static_cast<const T *>(p.q) + (it.r0 + tok) * p.ldq + (long long)head * D;

@@ -1,4 +1,4 @@
-"""pq_attn_mod at the ends of what it takes: caps far above the scores, slopes that are no numbers.
+"""pq_attn_mod at the ends of what it takes: caps far above the scores, slopes whose bias overflows f32 or that are no numbers.
 
 Bounds as in test_gpu_attn.py: 4e-5 for the scores (times `wide`, how much larger than usual they are), 2^-11 for the weights
 of 16-bit rows, the output's own rounding.  The cap's error is 2^-21 of a capped score (below 16 * wide times log2 e), or
@@ -89,6 +89,27 @@ def test_large_caps_beside_biases_and_views(dt, heads, news, ws):  # noqa: F811
     check(*attend(c, news, dt, n_q, ws, cap=1e6, slope=modref.slopes(n_q)), dt, off=off + bias)
     first = np.random.default_rng(23).integers(0, 650, n).astype(np.int32)
     check(*attend(c, news, dt, n_q, ws, cap=1e6, first=first, prefix=np.full(n, 640, np.int32), window=90, sinks=20), dt, off=off)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("news", NEWS)
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_slopes_whose_bias_overflows(dt, heads, news, cap, ws):  # noqa: F811
+    # the nearest token alone, or with a negative slope the farthest: distances go to 3000, 1.2e35 * 3000 is past f32
+    n_q, n_kv, d = heads
+    c = kvref.Cache(1, [3000], n_kv, 32, d, seed=24)
+    n = 1 if news is None else news[0]
+    slope = np.array([1.2e35, -1.2e35, 3e38, 1.0, 1e36, -3e38, 0.0, -1e36], np.float32)[:n_q]
+    off = (2.0 ** -21 * LOG2E * (16 if dt == "f32" else max(cap, 16)) if cap else 0.0) + 3 * 2.0 ** -24 * LOG2E * 64
+    check(*attend(c, news, dt, n_q, ws, cap=cap, slope=slope), dt, off=off)
+    # rows that see nothing but what lies ahead of them, or nothing at all
+    pos = np.arange(3000 - n, 3000)
+    args = dict(first=(pos + 2).astype(np.int32), prefix=np.full(n, 3000, np.int32))
+    check(*attend(c, news, dt, n_q, ws, cap=cap, slope=slope, **args), dt, off=off + 3 * 2.0 ** -24 * LOG2E * 2 * n)
+    # and the page of the nearest ones is not there
+    c.table[0, -4:] = -1
+    check(*attend(c, news, dt, n_q, ws, cap=cap, slope=slope), dt, off=off + 3 * 2.0 ** -24 * LOG2E * 128)
 
 
 @pytest.mark.parametrize("dt", DTS)
