@@ -407,7 +407,8 @@ size_t pq_attn_ws_bytes(int n_q, int n_kv, int d);
  * So first[r] is where the row's document begins when several lie in one
  * sequence, and prefix[r] the end of what all rows see, before them or after.
  * A row at a position below 0 sees nothing.  window and n_sink count from the
- * row's position and the sequence's first token, as in pq_attn.
+ * row's position and the sequence's first token, as in pq_attn.  At head sizes 64 and
+ * 128 a call with first or prefix whose row_start decreases somewhere writes nothing.
  *   cap     0, or from 2^-60 to 2^60
  *   slope   device f32 [n_q], or NULL; of any sign, magnitudes above 2^96 count
  *           as 2^96 (a row that sees something is NaN where its is not finite)

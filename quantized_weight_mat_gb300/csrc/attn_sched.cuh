@@ -189,6 +189,11 @@ template <int RT, int KT, int COST, bool MOD> struct UnitWalk {
 
 // Whether attn_bounds has run for the call.
 __device__ __forceinline__ bool counted(const AttnArgs &p) { return p.c.row_start && (p.mod.first || p.mod.prefix); }
+// Whether the rows of sequence s end before they begin (as seq_rows takes them): others then share rows, and the places that
+// attn_bounds has for their row tiles, so that its counts need not be those of the bounds that are left there.
+__device__ __forceinline__ bool rows_fall(const KvView &c, int s) {
+    return min(max(c.row_start[s + 1], 0), c.n_rows) < min(max(c.row_start[s], 0), c.n_rows);
+}
 
 // Places of the whole call, by one warp; lane 0's `walk` of every group of 32
 // sequences is not kept.
@@ -237,8 +242,10 @@ template <class Walk, int LEAST>
 __device__ __forceinline__ Cut find_range(const AttnArgs &p, Walk &walk, long long &first, long long &last) {
     const int lane = threadIdx.x & 31, n_seq = p.c.n_seq;
     long long total = 0, incl = 0, mine = 0;
+    bool fall = false;
     for (int s = 0; s < n_seq; s += 32) {
         mine = warp_places(p, s, walk, lane);
+        if (Walk::kMod && counted(p)) fall |= s + lane < n_seq && rows_fall(p.c, s + lane);
         incl = mine;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
@@ -248,6 +255,7 @@ __device__ __forceinline__ Cut find_range(const AttnArgs &p, Walk &walk, long lo
         incl += total;
         total = __shfl_sync(0xffffffffu, incl, 31);
     }
+    if (Walk::kMod && __any_sync(0xffffffffu, fall)) total = 0;
     const Cut cut = Cut::make<LEAST>(total * p.c.n_kv, p.grid);
     first = last = 0;
     if (total == 0 || (int)blockIdx.x >= cut.grid) return cut;

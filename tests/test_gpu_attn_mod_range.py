@@ -131,5 +131,27 @@ def test_a_slope_that_is_no_number_spoils_its_own_head(dt, heads, news, ws):  # 
         check(got[:, ~bad], ref[:, ~bad], vmax[:, ~bad], dt, off=3 * 2.0 ** -24 * LOG2E * (64 + 7))
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("starts", [[0, 200, 50, 300], [300, 0, 300, 300], [0, 9, 3, 12], [0, 400, -5, 300]])
+def test_rows_that_fall(dt, d, starts, ws):  # noqa: F811
+    # sequences share rows, against the rule: nothing is written, and the next call is as ever
+    import torch
+    c = kvref.Cache(3, [900, 700, 800], 2, 32, d, seed=26)
+    _, h = upload(c)
+    n, w = 300, 8 * d
+    q = torch.randn(n, w, device="cuda").to(tdt(dt))
+    first = dev(np.random.default_rng(26).integers(0, 900, n).astype(np.int32))
+    size = pq.pq_attn_mod_ws_bytes(8, 2, d, n, 3)
+    outs = []
+    for rows in ([0, 100, 200, 300], starts, [0, 100, 200, 300]):
+        out = torch.full((n, w), 99.0, dtype=q.dtype, device="cuda")
+        pq.pq_attn_mod(h, dev(np.array(rows, np.int32)), n, dt, q, w, 8, 0.1, 0, 0, pq.pq_score_mod(20.0, None, first), out, w, ws, size)
+        torch.cuda.synchronize()
+        outs.append(out)
+    assert torch.equal(outs[0], outs[2]) and not bool((outs[0] == 99.0).any())
+    assert bool((outs[1] == 99.0).all())
+
+
 def test_no_wait_ran_out():
     assert pq.pq_wait_timeouts() == 0
