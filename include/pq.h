@@ -416,8 +416,9 @@ size_t pq_attn_ws_bytes(int n_q, int n_kv, int d);
  * mod is plain host memory, read during the call only; NULL, or one without
  * any of the four, is pq_attn.  Everything else, the accuracy included, is as in
  * pq_attn, but for the cap's own error: 2^-21 of a capped score in calls of f32
- * rows and for caps above 256, 2^-20 of the cap in the others; the bias is rounded
- * to f32.  ws: at least pq_attn_mod_ws_bytes(...) bytes.
+ * rows and for caps above 256, 2^-20 of the cap in the others; and but for three
+ * roundings to f32 of the bias (in prompts of that of a token up to 15 farther).
+ * ws: at least pq_attn_mod_ws_bytes(...) bytes.
  */
 typedef struct pq_score_mod {
     float cap;

@@ -35,7 +35,7 @@
 // table, TMA) and 2.5 in the second kernel.  More warps of 16 tokens each: 78 us against 64.
 //
 // pq_attn_mod (MOD) changes scores and views between the two products: one row over 4096 tokens, capped, 13.1 us (12.2
-// without), 64 ragged sequences biased by distance 69 (67), windowed steps capped 47.8 (47.2): the loop waits on latency, and the loads
+// without), 64 ragged sequences biased by distance 69.8 (67), windowed steps capped 47.7 (47.2): the loop waits on latency, and the loads
 // hide only part of the instructions. What is asked is a template argument: read at run time, 73 and 49. Large caps, whose
 // scores take the form with a relative error: 49.4 windowed.
 //

@@ -49,9 +49,9 @@
 // decode kernel takes them, they are at 2.1e-4, but the second P V and the packing cost
 // 2048 rows over 10240 tokens 317 us instead of 248 and the windowed prompts 97 instead of 83.
 // The products cut their sums off towards zero: O ends up to 6e-5 short over 131072 tokens, a third of an f16 rounding.
-// pq_attn_mod (MOD): 32 columns at a time, so that code fetch keeps up (a cap over 64: 573 us where 32 took 470), those that
+// pq_attn_mod (MOD): 32 columns at a time (a cap over 64: 445 us where 32 took 433: code fetch), those that
 // nobody sees passed over, biased items from the row's own token back. Capped scores cost 14 cycles a pair in the
-// multipliers and 14 in the exponentials' unit, see kNearCap: the same 2048 rows 433 us; two halves' weights, which run side by
+// multipliers and 14 in the exponentials' unit, see kNearCap: the same 2048 rows 430 us; two halves' weights, which run side by
 // side, take 3500 cycles of a tile's 6400. Packed documents (2 x 4096 rows, about 700 tokens each) 169 us, a third of it the starts
 // and ends of items of 4 tiles.
 // Tiles at an edge of some row's view take the same step with a mask; tiles

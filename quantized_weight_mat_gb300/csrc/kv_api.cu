@@ -182,7 +182,9 @@ int attend(const pq_kv_cache *cache, const int *row_start, int n_rows, pq_dtype 
     cudaError_t e;
     // 16-bit rows: the wide kernel (256 rows at a time) from more than 32 rows per sequence and kv head. 16 sequences
     // of 2048 tokens, bf16, head size 128: 16 rows 30.1 us (narrow) against 41.9 (wide), 32 rows 43.3 against 42.4, 64 rows
-    // 69.7 against 43.9; head size 64: 28 rows 13.7 against 18.1, 56 rows 18.8 against 18.3. f32 rows keep the pair of fp16
+    // 69.7 against 43.9; head size 64: 28 rows 13.7 against 18.1, 56 rows 18.8 against 18.3. Capped scores, the same sequences:
+    // 32 rows 47.9 against 52.8, 48 rows 64.6 against 53.9; head size 64: 35 rows 17.9 against 22.3, 56 rows 21.5 against 22.4.
+    // So at head size 64 the narrow kernel would stay ahead up to some 50 rows; one limit serves both. f32 rows keep the pair of fp16
     // for q and for the weights that only the narrow one has.
     const bool wide = dt != PQ_F32 && rows > 32;
     if (c.d != 64 && c.d != 128) e = launch_attn_generic((int)dt, a, stream);

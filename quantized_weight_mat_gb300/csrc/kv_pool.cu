@@ -11,7 +11,9 @@
 //
 // In CUDA graphs: a fork of 3 sequences 2.5 us, of 224 with 72 entries each 4.3; pages given back 2.1 to 2.9 us; a
 // reservation that lacks nothing 4.3 us, its moving kernel 1.0 of it; 48128 pages for 256 sequences in a pool of 314858
-// 15.7; a compaction without a move 6.2. Each is a chain of four to ten trips to L2.
+// 15.7; a compaction without a move 6.2. Each is a chain of four to ten trips to L2. Lists of sequences are searched for equal
+// numbers by comparing each with all before it, which counts from some 10000 on: a fork of 4096 pairs 25 us, of 16384 98, of
+// 65536 1110; 65536 rows given back 530 with a list, 210 without.
 
 #include <climits>
 #include <cooperative_groups.h>
